@@ -598,6 +598,214 @@ int dpopt_reduce_adam_buckets_when_ready(const void *const *slice_table, int gra
                                          float lr, float beta1, float beta2, float eps,
                                          int64_t step, dpopt_stream_t stream);
 
+/* ------------------------------------------------------------------------- */
+/* Training-side operators: activation checkpoints, block join, token loss    */
+/* ------------------------------------------------------------------------- */
+
+/* What stands between two of the step's gradients: the residual join of a
+ * transformer block, the activations kept for the backward pass ("Глава 4.4",
+ * section 7: activation memory), the weight gradients that fill the replica
+ * buffers, and the loss whose gradient carries the loss scale.
+ *
+ * Conventions on top of those above.  `dtype` is a dpopt_grad_dtype.  A matrix
+ * is rows x cols with unit column stride and a row stride `ld` in elements (ld
+ * >= cols; not looked at for one row); any element-aligned address is accepted,
+ * and rows whose addresses and strides are multiples of 16 bytes take the
+ * vectorised path.  Arithmetic is in fp32 or wider whatever the types; a value
+ * is rounded to nearest even once, when it is stored.  Written arrays must not
+ * overlap one another or what the call reads, except where an entry names an
+ * in-place form (DPOPT_ERR_INVALID_ARG).  Zero rows are valid: matrices are
+ * then left alone, and sums over rows are written as zeros.  Infinities and NaN
+ * propagate.  Results are bitwise reproducible: every sum has a fixed order that
+ * depends on the sizes only. */
+
+/* Activations in 8 bits.  Blocks of DPOPT_ACT8_BLOCK consecutive columns of a
+ * row (the last block of a row may be short) share a power of two,
+ *   e     = max(floor(log2(max |x|)) - 6, lowest)   lowest: -24 for fp16, else -126
+ *   code  = clamp(round_half_even(x * 2^-e), -127, 127)        one signed byte
+ *   value = code * 2^e
+ * stored as the byte e + 127 per block.  |value - x| <= 2^e / 2 for |x| <= 127.5 *
+ * 2^e and <= 2^e above; 8.25 bits per element.  Every value is exact in the
+ * 16-bit type it came from, so products formed from a checkpoint see no second
+ * rounding.  A block holding an Inf or NaN is stored as byte 255 and reads back
+ * as NaN in all its elements, so that an overflow still reaches the gradients'
+ * overflow test.  An all-zero block has the lowest exponent. */
+#define DPOPT_ACT8_BLOCK 32
+
+/* Pack x (rows x cols of dtype) into codes (rows x cols bytes, row stride
+ * ld_codes) and exps (rows x ceil(cols / 32) bytes, row stride ld_exps).
+ * Errors: DPOPT_ERR_INVALID_ARG for negative sizes, an unknown dtype, null or
+ * misaligned pointers, strides below the widths, overlapping arrays. */
+int dpopt_act8_pack(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                    int8_t *codes, int64_t ld_codes, uint8_t *exps, int64_t ld_exps,
+                    dpopt_stream_t stream);
+
+/* The values of a packed matrix in `dtype`.  A value outside fp16's range, which
+ * an fp16 activation never gives, rounds as any other (to Inf above it). */
+int dpopt_act8_unpack(const int8_t *codes, int64_t ld_codes, const uint8_t *exps, int64_t ld_exps,
+                      int64_t rows, int64_t cols, void *x, int dtype, int64_t ldx,
+                      dpopt_stream_t stream);
+
+/* Weight gradient of a linear layer y = x W^T from the packed x:
+ *   dw[i][j] = sum_t dy[t][i] * value(t, j)  (+ addend[i][j]),   i < n, j < k
+ *  dy              tokens x n, bf16 or fp16 (dtype; fp32: DPOPT_ERR_UNSUPPORTED).
+ *  codes, exps     the packed x, tokens x k; x was of type `dtype`, so that its
+ *                  values are exact operands of the products.
+ *  dw              n x k of out_dtype, written.
+ *  addend          NULL, or n x k of out_dtype: a gradient to add to (gradients
+ *                  accumulated over micro-batches).  May be dw itself with the
+ *                  same stride.
+ *  scratch         DEVICE, 256-byte aligned, dpopt_act8_wgrad_scratch_bytes()
+ *                  bytes, overlapping no other array.
+ * Products are summed in fp32.  tokens = 0 writes the addend, or zeros.
+ * Errors: as above, DPOPT_ERR_INVALID_ARG for too small a scratch, and
+ * DPOPT_ERR_UNSUPPORTED for a size of 2^31 or more. */
+int dpopt_act8_wgrad(const void *dy, int dtype, int64_t ld_dy, const int8_t *codes,
+                     int64_t ld_codes, const uint8_t *exps, int64_t ld_exps, int64_t tokens,
+                     int64_t n, int64_t k, void *dw, int out_dtype, int64_t ld_dw,
+                     const void *addend, int64_t ld_addend, void *scratch, int64_t scratch_bytes,
+                     dpopt_stream_t stream);
+int dpopt_act8_wgrad_scratch_bytes(int64_t tokens, int64_t n, int64_t k, int64_t *bytes_out);
+
+/* A matrix, and a packed matrix, of an operator's argument block. */
+typedef struct {
+    void *data; /* NULL: absent */
+    int64_t ld;
+} dpopt_matrix;
+
+typedef struct {
+    int8_t *codes; /* NULL: absent */
+    int64_t ld_codes;
+    uint8_t *exps;
+    int64_t ld_exps;
+} dpopt_act8;
+
+/* The join between two blocks: the norm after the block just run, its gate and
+ * the residual scale, and the norm before the next block, in one pass.  With h
+ * the residual stream and y the block's output, for each row
+ *   z     = y * rstd_post * w_post      rstd_post = 1 / sqrt(mean(y^2) + eps)
+ *   h_out = res_scale * h + branch_scale * gate * z
+ *   u     = h_out * rstd_pre * w_pre    rstd_pre = 1 / sqrt(mean(h_out^2) + eps)
+ * Each part may be left out: rstd_post NULL: no norm after the block (z = y, and
+ * w_post must be NULL); w_post, w_pre, gate NULL: ones; u NULL: no norm before
+ * the next block (then rstd_pre and w_pre must be NULL).  u and rstd_pre are
+ * formed from h_out before it is rounded.  The optional packed outputs are the
+ * 8-bit checkpoints of y, of h_out and of u as stored (bit for bit what
+ * dpopt_act8_pack makes of those arrays).
+ *  gate            gate_rows = 0: one row of cols values for every row (a gate or
+ *                  layer scale per channel); gate_rows = R > 0: row t uses gate row
+ *                  t / R, ceil(rows / R) rows (a gate per sequence, or with R = 1
+ *                  per element).
+ *  h_out           may be h itself with the same stride (in place).
+ *  param_dtype     type of w_post, w_pre and gate.
+ * Errors: DPOPT_ERR_INVALID_ARG for a null args, h, y or h_out, eps not finite
+ * or negative, non-finite scales, and as above; DPOPT_ERR_UNSUPPORTED for cols >
+ * DPOPT_JOIN_MAX_COLS. */
+#define DPOPT_JOIN_MAX_COLS 16384
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype, param_dtype;
+    float eps, res_scale, branch_scale;
+    int32_t reserved; /* 0 */
+    int64_t gate_rows;
+    dpopt_matrix h, y, gate, h_out, u;
+    const void *w_post, *w_pre;  /* cols values each */
+    float *rstd_post, *rstd_pre; /* rows values each, written */
+    dpopt_act8 y8, h8, u8;       /* written where present */
+} dpopt_block_join_args;
+int dpopt_block_join(const dpopt_block_join_args *args, dpopt_stream_t stream);
+
+/* The join's gradient.  With dh_out the gradient reaching h_out along the
+ * residual stream and du the one reaching u (absent: no norm before the next
+ * block), and C = cols,
+ *   d      = dh_out + rstd_pre * (w_pre*du - h_out * rstd_pre^2 * <w_pre*du, h_out> / C)
+ *   dh     = res_scale * d
+ *   dz     = branch_scale * gate * d
+ *   dy     = rstd_post * (w_post*dz - y * rstd_post^2 * <w_post*dz, y> / C)   (or dz)
+ *   dw_pre  = sum_t du * h_out * rstd_pre        dw_post = sum_t dz * y * rstd_post
+ *   dgate   = sum over the rows of a gate row of branch_scale * z * d
+ * from the statistics that the forward call stored.  y and h_out come either as
+ * matrices or as their 8-bit checkpoints (y8, h8; exactly one of the two; h_out
+ * only with du), whose values then stand for them.
+ *  dh              may be dh_out itself with the same stride, or absent.
+ *  dw_post, dw_pre, dgate  of param_dtype; each NULL or absent if not wanted; dw_post
+ *                  needs rstd_post, dw_pre needs du, dgate needs a gate (rows as
+ *                  there).
+ *  scratch         DEVICE, 256-byte aligned,
+ *                  dpopt_block_join_scratch_bytes() bytes.
+ * Other arguments and errors as for dpopt_block_join. */
+typedef struct {
+    int64_t rows, cols;
+    int32_t dtype, param_dtype;
+    float res_scale, branch_scale;
+    int64_t gate_rows;
+    dpopt_matrix dh_out, du, y, h_out, gate, dh, dy, dgate;
+    dpopt_act8 y8, h8;
+    const void *w_post, *w_pre;
+    const float *rstd_post, *rstd_pre;
+    void *dw_post, *dw_pre; /* cols values each */
+    void *scratch;
+    int64_t scratch_bytes;
+} dpopt_block_join_grad_args;
+int dpopt_block_join_backward(const dpopt_block_join_grad_args *args, dpopt_stream_t stream);
+int dpopt_block_join_scratch_bytes(int64_t rows, int64_t cols, int64_t gate_rows,
+                                   int64_t *bytes_out);
+
+/* Log probabilities of given tokens under softmax(logits * inv_temperature), with
+ * entropy and top alternatives.  For each row, with m = max_j x_j, s_j = (x_j - m)
+ * * inv_temperature and L = log sum_j exp(s_j):
+ *   logprob[i]      = s_tok - L for tok = tokens[row][i]; 0 for a negative token
+ *                     (none given); NaN for a token >= vocab
+ *   stats           = (m, L), two floats per row, what the gradient needs
+ *   entropy         = L - sum_j p_j s_j,   p_j = exp(s_j - L)
+ *   top_index[i], top_logprob[i]: the `top` largest logits and their log
+ *                     probabilities, largest first, among equals the lowest index
+ *                     first (a NaN counts as larger than any number)
+ * A logit of -Inf is a masked entry: probability 0, nothing added to the entropy.
+ * A row with every entry -Inf has m = -Inf, L = 0, log probabilities -Inf, entropy 0.
+ * A row with a NaN or +Inf has L = NaN and NaN results.
+ *  logits          rows x vocab of dtype, row stride ld; vocab >= 1.
+ *  tokens          rows x n_tokens, contiguous, 0 <= n_tokens <= DPOPT_MAX_TOKENS.
+ *  logprob         rows x n_tokens, contiguous (NULL when n_tokens is 0).
+ *  entropy         rows values, or NULL.
+ *  top             0 <= top <= min(vocab, DPOPT_MAX_TOP); top_logprob and top_index
+ *                  rows x top, contiguous (NULL when top is 0).
+ *  scratch         DEVICE, 256-byte aligned, dpopt_token_logprob_scratch_bytes()
+ *                  bytes (which may be 0).
+ * Errors: DPOPT_ERR_INVALID_ARG as above, for a non-finite or non-positive
+ * inv_temperature or a `top` or n_tokens out of range; DPOPT_ERR_UNSUPPORTED for
+ * vocab >= 2^31. */
+#define DPOPT_MAX_TOKENS 64
+#define DPOPT_MAX_TOP 32
+int dpopt_token_logprob(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                        const int64_t *tokens, int n_tokens, float inv_temperature,
+                        float *logprob, float *stats, float *entropy, int top,
+                        float *top_logprob, int64_t *top_index, void *scratch,
+                        int64_t scratch_bytes, dpopt_stream_t stream);
+int dpopt_token_logprob_scratch_bytes(int64_t rows, int64_t vocab, int top, int64_t *bytes_out);
+
+/* Gradient of sum(dlogprob * logprob) + sum(dentropy * entropy) with respect to the
+ * logits, times the loss scale:
+ *   dlogits_j = scale * inv_temperature * ( sum_i dlogprob[i] * ([j = tok_i] - p_j)
+ *                                           - dentropy * p_j * (log p_j + entropy) )
+ * in the logits' type; masked entries get 0.  Negative tokens add nothing, a token
+ * >= vocab makes the row NaN, and a row with every entry masked gets zeros.
+ *  stats           rows x 2, as dpopt_token_logprob stored them.
+ *  dlogprob        rows x n_tokens, contiguous.
+ *  entropy, dentropy  rows values each, both or neither (NULL).
+ *  loss_scale      NULL (scale 1), or the DEVICE state of dynamic loss scaling
+ *                  (dpopt_loss_scale_init), whose current scale is read when the
+ *                  kernel runs.
+ *  dlogits         rows x vocab of dtype, row stride ld_dlogits; may be logits itself
+ *                  with the same stride (in place). */
+int dpopt_token_logprob_backward(const void *logits, int dtype, int64_t rows, int64_t vocab,
+                                 int64_t ld, const int64_t *tokens, int n_tokens,
+                                 float inv_temperature, const float *stats,
+                                 const float *dlogprob, const float *entropy,
+                                 const float *dentropy,
+                                 const dpopt_loss_scale_state *loss_scale, void *dlogits,
+                                 int64_t ld_dlogits, dpopt_stream_t stream);
+
 /* Wait for `stream`, then return and clear the current device's status word:
  * DPOPT_OK, or DPOPT_ERR_TIMEOUT if a bounded device-side wait gave up since the
  * last call, or DPOPT_ERR_CUDA if the wait itself failed; in the bounds-checked

@@ -15,5 +15,10 @@ from .binding import (  # noqa: F401
     reduce_adamw, reduce_adamw_buckets,
     step_options, stream_status,
 )
+from .operators import (  # noqa: F401
+    act8_empty, act8_pack, act8_unpack, act8_wgrad, act8_wgrad_scratch_bytes, block_join,
+    block_join_backward, block_join_scratch_bytes, token_logprob, token_logprob_backward,
+    token_logprob_scratch_bytes,
+)
 
 __version__ = "0.1.0"

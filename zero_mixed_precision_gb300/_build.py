@@ -1,8 +1,10 @@
 """Compile the CUDA library in-tree for sm_103a (the only target).
 
 The library is several translation units compiled in parallel and linked
-into one shared object: the C ABI (dpopt.cu), the bulk-copy kernel (tma.cu)
-and the kernels of each gradient type (launch_gk.cu, once per type)."""
+into one shared object: the step's C ABI (dpopt.cu), the bulk-copy kernel
+(tma.cu), the kernels of each gradient type (launch_gk.cu, once per type) and
+the training-side operators (act8.cu, act8_wgrad.cu, block_join.cu,
+token_logprob.cu)."""
 from __future__ import annotations
 
 import os
@@ -35,6 +37,10 @@ UNITS = [
     ("step_bf16", "launch_gk.cu", ["-DDPOPT_GK=0"]),
     ("step_f32", "launch_gk.cu", ["-DDPOPT_GK=1"]),
     ("step_f16", "launch_gk.cu", ["-DDPOPT_GK=2"]),
+    ("act8", "act8.cu", []),
+    ("act8_wgrad", "act8_wgrad.cu", []),
+    ("block_join", "block_join.cu", []),
+    ("token_logprob", "token_logprob.cu", []),
 ]
 SOURCES = sorted({os.path.join(CSRC, src) for _, src, _ in UNITS})
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)

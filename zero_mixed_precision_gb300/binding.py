@@ -79,6 +79,43 @@ class LossScaleConfig(ctypes.Structure):
 
 _PCFG = ctypes.POINTER(LossScaleConfig)
 
+
+class Matrix(ctypes.Structure):
+    """dpopt_matrix."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class Act8(ctypes.Structure):
+    """dpopt_act8."""
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("exps", ctypes.c_void_p), ("ld_exps", ctypes.c_int64)]
+
+
+class BlockJoinArgs(ctypes.Structure):
+    """dpopt_block_join_args."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("gate_rows", ctypes.c_int64),
+                *[(n, Matrix) for n in ("h", "y", "gate", "h_out", "u")],
+                *[(n, ctypes.c_void_p) for n in ("w_post", "w_pre", "rstd_post", "rstd_pre")],
+                *[(n, Act8) for n in ("y8", "h8", "u8")]]
+
+
+class BlockJoinGradArgs(ctypes.Structure):
+    """dpopt_block_join_grad_args."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("res_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("gate_rows", ctypes.c_int64),
+                *[(n, Matrix) for n in ("dh_out", "du", "y", "h_out", "gate", "dh", "dy",
+                                        "dgate")],
+                *[(n, Act8) for n in ("y8", "h8")],
+                *[(n, ctypes.c_void_p) for n in ("w_post", "w_pre", "rstd_post", "rstd_pre",
+                                                 "dw_post", "dw_pre", "scratch")],
+                ("scratch_bytes", ctypes.c_int64)]
+
 _SIGS = {
     "dpopt_reduce_adam": ([_PP, _I, _I64, _I, _I64, _P, _P, _P, _P, _F, _F, _F, _F, _I64, _P], _I),
     "dpopt_reduce_adam_ex": ([_PP, _I, _I, _I64, _I, _I64, _P, _P, _P, _P, _F, _F, _F, _F, _I64,
@@ -131,6 +168,19 @@ _SIGS = {
     "dpopt_get_gather_policy": ([], _I),
     "dpopt_selftest_wait_timeout": ([_I64, _P], _I),
     "dpopt_selftest_bounds": ([_P], _I),
+    "dpopt_act8_pack": ([_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _P], _I),
+    "dpopt_act8_unpack": ([_P, _I64, _P, _I64, _I64, _I64, _P, _I, _I64, _P], _I),
+    "dpopt_act8_wgrad": ([_P, _I, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I, _I64, _P,
+                          _I64, _P, _I64, _P], _I),
+    "dpopt_act8_wgrad_scratch_bytes": ([_I64, _I64, _I64, _PI64], _I),
+    "dpopt_block_join": ([ctypes.POINTER(BlockJoinArgs), _P], _I),
+    "dpopt_block_join_backward": ([ctypes.POINTER(BlockJoinGradArgs), _P], _I),
+    "dpopt_block_join_scratch_bytes": ([_I64, _I64, _I64, _PI64], _I),
+    "dpopt_token_logprob": ([_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _I, _P, _P, _P,
+                             _I64, _P], _I),
+    "dpopt_token_logprob_scratch_bytes": ([_I64, _I64, _I, _PI64], _I),
+    "dpopt_token_logprob_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _P, _P, _P,
+                                      _I64, _P], _I),
 }
 
 for _name, (_args, _res) in _SIGS.items():
@@ -454,6 +504,69 @@ def dpopt_get_gather_policy() -> int:
 
 def dpopt_selftest_wait_timeout(limit_cycles: int, stream: int = 0) -> int:
     return _lib.dpopt_selftest_wait_timeout(limit_cycles, stream)
+
+
+def dpopt_act8_pack(x: int, dtype: int, rows: int, cols: int, ldx: int, codes: int, ld_codes: int,
+                    exps: int, ld_exps: int, stream: int = 0) -> int:
+    return _lib.dpopt_act8_pack(x, dtype, rows, cols, ldx, codes, ld_codes, exps, ld_exps, stream)
+
+
+def dpopt_act8_unpack(codes: int, ld_codes: int, exps: int, ld_exps: int, rows: int, cols: int,
+                      x: int, dtype: int, ldx: int, stream: int = 0) -> int:
+    return _lib.dpopt_act8_unpack(codes, ld_codes, exps, ld_exps, rows, cols, x, dtype, ldx, stream)
+
+
+def dpopt_act8_wgrad(dy: int, dtype: int, ld_dy: int, codes: int, ld_codes: int, exps: int,
+                     ld_exps: int, tokens: int, n: int, k: int, dw: int, out_dtype: int,
+                     ld_dw: int, addend: int, ld_addend: int, scratch: int, scratch_bytes: int,
+                     stream: int = 0) -> int:
+    return _lib.dpopt_act8_wgrad(dy, dtype, ld_dy, codes, ld_codes, exps, ld_exps, tokens, n, k, dw,
+                                 out_dtype, ld_dw, addend, ld_addend, scratch, scratch_bytes,
+                                 stream)
+
+
+def dpopt_act8_wgrad_scratch_bytes(tokens: int, n: int, k: int) -> tuple[int, int]:
+    out = ctypes.c_int64(0)
+    rc = _lib.dpopt_act8_wgrad_scratch_bytes(tokens, n, k, ctypes.byref(out))
+    return rc, out.value
+
+
+def dpopt_block_join(args: BlockJoinArgs | None, stream: int = 0) -> int:
+    return _lib.dpopt_block_join(ctypes.byref(args) if args is not None else None, stream)
+
+
+def dpopt_block_join_backward(args: BlockJoinGradArgs | None, stream: int = 0) -> int:
+    return _lib.dpopt_block_join_backward(ctypes.byref(args) if args is not None else None, stream)
+
+
+def dpopt_block_join_scratch_bytes(rows: int, cols: int, gate_rows: int) -> tuple[int, int]:
+    out = ctypes.c_int64(0)
+    rc = _lib.dpopt_block_join_scratch_bytes(rows, cols, gate_rows, ctypes.byref(out))
+    return rc, out.value
+
+
+def dpopt_token_logprob(logits: int, dtype: int, rows: int, vocab: int, ld: int, tokens: int,
+                        n_tokens: int, inv_temperature: float, logprob: int, stats: int,
+                        entropy: int, top: int, top_logprob: int, top_index: int, scratch: int,
+                        scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.dpopt_token_logprob(logits, dtype, rows, vocab, ld, tokens, n_tokens,
+                                    inv_temperature, logprob, stats, entropy, top, top_logprob,
+                                    top_index, scratch, scratch_bytes, stream)
+
+
+def dpopt_token_logprob_scratch_bytes(rows: int, vocab: int, top: int) -> tuple[int, int]:
+    out = ctypes.c_int64(0)
+    rc = _lib.dpopt_token_logprob_scratch_bytes(rows, vocab, top, ctypes.byref(out))
+    return rc, out.value
+
+
+def dpopt_token_logprob_backward(logits: int, dtype: int, rows: int, vocab: int, ld: int,
+                                 tokens: int, n_tokens: int, inv_temperature: float, stats: int,
+                                 dlogprob: int, entropy: int, dentropy: int, loss_scale: int,
+                                 dlogits: int, ld_dlogits: int, stream: int = 0) -> int:
+    return _lib.dpopt_token_logprob_backward(logits, dtype, rows, vocab, ld, tokens, n_tokens,
+                                             inv_temperature, stats, dlogprob, entropy, dentropy,
+                                             loss_scale, dlogits, ld_dlogits, stream)
 
 
 # ---------------------------------------------------------------------------

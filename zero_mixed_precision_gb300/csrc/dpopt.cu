@@ -55,6 +55,8 @@ std::once_flag g_bounds_once[kMaxDevices];
 unsigned int* g_bounds_addr[kMaxDevices];
 cudaError_t g_bounds_err[kMaxDevices];
 
+}  // namespace
+
 unsigned int* bounds_status_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -65,6 +67,8 @@ unsigned int* bounds_status_word() {
   });
   return g_bounds_err[dev] == cudaSuccess ? g_bounds_addr[dev] : nullptr;
 }
+
+namespace {
 
 __global__ void bounds_selftest_kernel(Hyper h, int64_t len) {
   // an index one past the end: the check fails, sets the word, and nothing

@@ -1,11 +1,12 @@
 // internal.h -- what the library's translation units share: the launch
 // parameter tables, the error helpers and the launchers each unit defines.
 //
-// The library is four units compiled in parallel: the C ABI and the small
-// kernels (dpopt.cu), the bulk-copy kernel (tma.cu) and the step, mixed-
+// The library's units are compiled in parallel: the C ABI of the step and the
+// small kernels (dpopt.cu), the bulk-copy kernel (tma.cu), the step, mixed-
 // precision step and squared-norm kernels of one gradient type
-// (launch_gk.cu, compiled once per type with -DDPOPT_GK=0|1|2).  Nothing here
-// allocates memory.
+// (launch_gk.cu, compiled once per type with -DDPOPT_GK=0|1|2) and the
+// training-side operators, each with its entries (act8.cu, act8_wgrad.cu,
+// block_join.cu, token_logprob.cu; ops.cuh).  Nothing here allocates memory.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -40,6 +41,10 @@ struct SegDesc {
 // Error reporting (message kept per host thread for dpopt_last_error).
 int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t e, const char* what);
+#ifdef DPOPT_DEBUG_BOUNDS
+// The current device's word that every failed index check sets.
+unsigned int* bounds_status_word();
+#endif
 // Counts a kernel launch of this host thread (dpopt_launch_count).
 void count_launch();
 // SM count of the current device, cached per device.

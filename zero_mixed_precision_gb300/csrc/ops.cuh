@@ -1,0 +1,360 @@
+// ops.cuh -- what the training-side operators share (block_join.cu, act8.cu,
+// act8_wgrad.cu, token_logprob.cu): element types, 8-element vectors, warp
+// sums, the 8-bit block format, bounds checks and host argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "internal.h"
+
+namespace dpopt {
+
+// ---------------------------------------------------------------------------
+// element types: every operator computes in fp32 and rounds to nearest even
+// once, when a value is stored
+// ---------------------------------------------------------------------------
+
+using bf16 = __nv_bfloat16;
+using fp16 = __half;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(fp16 x) { return __half2float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ fp16 from_f32<fp16>(float x) { return __float2half_rn(x); }
+
+// Element i of an array whose type is known only at run time (weights, gates
+// and parameter gradients: a dpopt_grad_dtype).  The branch is uniform.
+__device__ __forceinline__ float ld_any(const void* p, int dtype, int64_t i) {
+  if (dtype == DPOPT_GRAD_BF16) return to_f32(static_cast<const bf16*>(p)[i]);
+  if (dtype == DPOPT_GRAD_F16) return to_f32(static_cast<const fp16*>(p)[i]);
+  return static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void st_any(void* p, int dtype, int64_t i, float x) {
+  if (dtype == DPOPT_GRAD_BF16)
+    static_cast<bf16*>(p)[i] = from_f32<bf16>(x);
+  else if (dtype == DPOPT_GRAD_F16)
+    static_cast<fp16*>(p)[i] = from_f32<fp16>(x);
+  else
+    static_cast<float*>(p)[i] = x;
+}
+
+// Eight consecutive elements at a 16-byte aligned address.
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, bf16) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, fp16) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, bf16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, fp16) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Raw 8-element vectors: 16 bytes of a 16-bit type, 32 bytes of fp32.
+template <class T>
+struct Raw8 {
+  uint4 v;
+};
+template <>
+struct Raw8<float> {
+  uint4 v, w;
+};
+
+template <class T>
+__device__ __forceinline__ Raw8<T> ld_raw8(const T* p) {
+  Raw8<T> r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
+               : "l"(p));
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w.x), "=r"(r.w.y), "=r"(r.w.z), "=r"(r.w.w)
+                 : "l"(p + 4));
+  }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    f[0] = __uint_as_float(r.v.x); f[1] = __uint_as_float(r.v.y);
+    f[2] = __uint_as_float(r.v.z); f[3] = __uint_as_float(r.v.w);
+    f[4] = __uint_as_float(r.w.x); f[5] = __uint_as_float(r.w.y);
+    f[6] = __uint_as_float(r.w.z); f[7] = __uint_as_float(r.w.w);
+  } else {
+    unpack2(r.v.x, f[0], f[1], T());
+    unpack2(r.v.y, f[2], f[3], T());
+    unpack2(r.v.z, f[4], f[5], T());
+    unpack2(r.v.w, f[6], f[7], T());
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void st_vec8(T* p, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    st_stream16(reinterpret_cast<float*>(p), f[0], f[1], f[2], f[3]);
+    st_stream16(reinterpret_cast<float*>(p) + 4, f[4], f[5], f[6], f[7]);
+  } else {
+    st_stream16u(p, pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
+                 pack2(f[6], f[7], T()));
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// the 8-bit block format (include/dpopt.h, dpopt_act8_pack)
+// ---------------------------------------------------------------------------
+
+constexpr int kAct8Block = DPOPT_ACT8_BLOCK;
+
+// Lowest exponent byte a type's blocks get: 2^-126 is the smallest normal
+// fp32; fp16 values are all multiples of 2^-24, so finer codes would add
+// nothing and 2^-24 keeps the scale itself an fp16 number.
+template <class T>
+__device__ __forceinline__ constexpr uint32_t act8_low_byte() {
+  return sizeof(T) == 2 && std::is_same_v<T, fp16> ? 127 - 24 : 127 - 126;
+}
+
+// Exponent byte of a block whose largest magnitude has the fp32 bits `amax`
+// (sign cleared; integer order is magnitude order and puts Inf and NaN last).
+template <class T>
+__device__ __forceinline__ uint32_t act8_byte(uint32_t amax) {
+  if (amax >= 0x7f800000u) return 255u;
+  const uint32_t e = amax >> 23;
+  constexpr uint32_t low = act8_low_byte<T>();
+  return e > low + 6 ? e - 6 : low;
+}
+// 2^-(byte - 127) and 2^(byte - 127): exact.  A block of byte 255 gets codes
+// of zero and unpacks to NaN.
+__device__ __forceinline__ float act8_inverse(uint32_t byte) {
+  return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float act8_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte << 23);
+}
+
+// Code of one value: |x| * inv < 128, clamped to 127, rounded to nearest even
+// by adding 1.5 * 2^23 (the low byte is then the code in two's complement).
+// inv = 0 marks a non-finite block: its codes are zero.
+__device__ __forceinline__ uint32_t act8_code(float x, float inv) {
+  const float s = fminf(fmaxf(x * inv, -127.f), 127.f);
+  return inv == 0.f ? 0u : (__float_as_uint(s + 12582912.f) & 0xffu);
+}
+
+// A packed matrix a kernel writes or reads (codes null: absent).
+struct Act8Out {
+  int8_t* codes;
+  int64_t ld_codes;
+  uint8_t* exps;
+  int64_t ld_exps;
+  int vec;  // codes may be moved 8 at a time
+};
+
+// Pack the eight values f of columns col.. of one row.  The four threads of a
+// block's 32 columns (adjacent lanes, the first at a multiple of four) call it
+// together; columns from `cols` on carry zeros and are not stored.
+template <class T>
+__device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int64_t col,
+                                            int64_t cols, const float (&f)[8]) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(f[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const uint32_t byte = act8_byte<T>(amax);
+  const float inv = act8_inverse(byte);
+  int8_t* dst = o.codes + row * o.ld_codes + col;
+  if (o.vec && col + 8 <= cols) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo |= act8_code(f[i], inv) << (8 * i);
+      hi |= act8_code(f[4 + i], inv) << (8 * i);
+    }
+    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) dst[i] = (int8_t)act8_code(f[i], inv);
+  }
+  if (col < cols && (threadIdx.x & 3) == 0)
+    o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
+}
+
+// Values of columns col.. of one row (zeros from `cols` on).
+__device__ __forceinline__ void act8_load8(const Act8Out& o, int64_t row, int64_t col,
+                                           int64_t cols, float (&f)[8]) {
+  const int8_t* src = o.codes + row * o.ld_codes + col;
+  const float scale = col < cols ? act8_scale(o.exps[row * o.ld_exps + col / kAct8Block]) : 0.f;
+  if (o.vec && col + 8 <= cols) {
+    const uint2 c = *reinterpret_cast<const uint2*>(src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = (float)(int8_t)(c.x >> (8 * i)) * scale;
+      f[4 + i] = (float)(int8_t)(c.y >> (8 * i)) * scale;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? (float)src[i] * scale : 0.f;
+  }
+}
+
+// A matrix a kernel reads or writes (data null: absent).
+struct Mat {
+  void* data;
+  int64_t ld;
+  int vec;  // rows may be moved 8 elements at a time
+};
+
+template <class T>
+__device__ __forceinline__ void mat_load8(const Mat& m, int64_t row, int64_t col, int64_t cols,
+                                          float (&f)[8]) {
+  const T* src = static_cast<const T*>(m.data) + row * m.ld + col;
+  if (m.vec && col + 8 <= cols) {
+    widen8<T>(ld_raw8<T>(src), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? to_f32(src[i]) : 0.f;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void mat_store8(const Mat& m, int64_t row, int64_t col, int64_t cols,
+                                           const float (&f)[8]) {
+  T* dst = static_cast<T*>(m.data) + row * m.ld + col;
+  if (m.vec && col + 8 <= cols) {
+    st_vec8<T>(dst, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) dst[i] = from_f32<T>(f[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bounds checks of the bounds-checked build
+// ---------------------------------------------------------------------------
+
+#ifdef DPOPT_DEBUG_BOUNDS
+// The device word a failed check sets, passed to every operator kernel.
+struct Dbg {
+  unsigned int* status;
+};
+inline Dbg make_dbg() { return Dbg{bounds_status_word()}; }
+__device__ __forceinline__ bool dbg_ok(const Dbg& d, bool cond) {
+  if (!cond && d.status) atomicOr(d.status, 1u);
+  return cond;
+}
+#else
+struct Dbg {};
+inline Dbg make_dbg() { return Dbg{}; }
+__device__ __forceinline__ constexpr bool dbg_ok(const Dbg&, bool) { return true; }
+#endif
+
+// ---------------------------------------------------------------------------
+// host argument checks
+// ---------------------------------------------------------------------------
+
+inline bool known_dtype(int d) {
+  return d == DPOPT_GRAD_BF16 || d == DPOPT_GRAD_F32 || d == DPOPT_GRAD_F16;
+}
+inline int64_t dtype_size(int d) { return d == DPOPT_GRAD_F32 ? 4 : 2; }
+
+// One array a call reads or writes: its name in messages, its byte range
+// [lo, hi) (empty for an absent one) and whether the call writes it.
+struct Span {
+  const char* name;
+  uintptr_t lo, hi;
+  bool written;
+};
+
+// A rows x cols matrix with row stride ld (elements of esize bytes).
+inline int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld,
+                        int64_t esize, bool written, Span* out) {
+  *out = Span{name, 0, 0, written};
+  if (rows == 0 || cols == 0) return DPOPT_OK;
+  if (!p) return fail(DPOPT_ERR_INVALID_ARG, "%s is null", name);
+  if ((uintptr_t)p % (uintptr_t)esize)
+    return fail(DPOPT_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+  if (ld < cols && rows > 1)
+    return fail(DPOPT_ERR_INVALID_ARG, "%s: row stride %lld is below its %lld columns", name,
+                (long long)ld, (long long)cols);
+  if (rows > 1 && ld > (INT64_MAX / 16 - cols) / rows)
+    return fail(DPOPT_ERR_INVALID_ARG, "%s: size out of range", name);
+  const int64_t elems = (rows - 1) * (rows > 1 ? ld : 0) + cols;
+  out->lo = (uintptr_t)p;
+  out->hi = (uintptr_t)p + (uintptr_t)(elems * esize);
+  if (out->hi < out->lo) return fail(DPOPT_ERR_INVALID_ARG, "%s: size out of range", name);
+  return DPOPT_OK;
+}
+
+// No written array may overlap another; two entries with the same start may
+// be declared the same array (an in-place form) by leaving one out.
+inline int check_overlaps(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if ((s[i].written || s[j].written) && s[i].lo < s[j].hi && s[j].lo < s[i].hi)
+        return fail(DPOPT_ERR_INVALID_ARG, "%s overlaps %s", s[i].name, s[j].name);
+  return DPOPT_OK;
+}
+
+#define DPOPT_TRY(expr)                      \
+  do {                                       \
+    const int try_rc_ = (expr);              \
+    if (try_rc_ != DPOPT_OK) return try_rc_; \
+  } while (0)
+
+// The kernel's view of a matrix / packed matrix argument, checked; spans go to
+// s[*n], s[*n + 1].
+inline int take_matrix(const char* name, const dpopt_matrix& m, int64_t rows, int64_t cols,
+                       int64_t esize, bool written, Mat* out, Span* s, int* n) {
+  DPOPT_TRY(check_matrix(name, m.data, rows, cols, m.ld, esize, written, &s[*n]));
+  ++*n;
+  *out = Mat{m.data, rows > 1 ? m.ld : cols,
+             (uintptr_t)m.data % 16 == 0 && (rows <= 1 || m.ld * esize % 16 == 0)};
+  return DPOPT_OK;
+}
+inline int take_act8(const char* name, const dpopt_act8& a, int64_t rows, int64_t cols,
+                     bool written, Act8Out* out, Span* s, int* n) {
+  DPOPT_TRY(check_matrix(name, a.codes, rows, cols, a.ld_codes, 1, written, &s[*n]));
+  ++*n;
+  DPOPT_TRY(check_matrix(name, a.exps, rows, (cols + kAct8Block - 1) / kAct8Block, a.ld_exps, 1,
+                          written, &s[*n]));
+  ++*n;
+  *out = Act8Out{a.codes, a.ld_codes, a.exps, a.ld_exps,
+                 (uintptr_t)a.codes % 8 == 0 && (rows <= 1 || a.ld_codes % 8 == 0)};
+  return DPOPT_OK;
+}
+
+// Ends a launch: its error, or a counted launch.
+inline int launched(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  count_launch();
+  return DPOPT_OK;
+}
+
+}  // namespace dpopt
