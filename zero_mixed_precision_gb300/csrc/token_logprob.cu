@@ -10,14 +10,37 @@ namespace {
 constexpr int kTokThreads = 256;
 constexpr int kTokWarps = kTokThreads / 32;
 
+// Rows are cut into parts, one CTA each, when there are too few rows to fill
+// the GPU: about kTokCtas CTAs in all, none below kTokPartMin elements.  A
+// function of the sizes alone, so results do not depend on the GPU.
+constexpr int kTokCtas = 512, kTokPartMin = 2048, kTokMaxParts = 64;
+
+__host__ __device__ inline int64_t tok_parts(int64_t rows, int64_t vocab) {
+  int64_t parts = rows >= kTokCtas ? 1 : kTokCtas / (rows > 0 ? rows : 1);
+  const int64_t most = (vocab + kTokPartMin - 1) / kTokPartMin;
+  parts = parts < most ? parts : most;
+  return parts < kTokMaxParts ? parts : kTokMaxParts;
+}
+
+// What one part of a row leaves for the join: the running softmax and, behind
+// it in scratch, its `top` largest entries.
+struct TokPartial {
+  float max, ref, sum, ent;
+};
+
 struct LogprobParams {
   int64_t rows, vocab, ld;
   const void* logits;
   const int64_t* tokens;
   int n_tokens, top;
   float inv_temp;
+  float c;  // inv_temp * log2(e)
+  int parts;
+  int64_t part_len;
   float *logprob, *stats, *entropy, *top_logprob;
   int64_t* top_index;
+  TokPartial* partial;  // [rows][parts]
+  uint64_t* keys;       // [rows][parts][top]
   Dbg dbg;
 };
 
@@ -26,18 +49,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-// Total order of (logit, index): larger logits first, among equals the lower
-// index, a NaN above every number.  -0 counts as +0.
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
-  uint32_t b = __float_as_uint(x + 0.f);
-  b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  if (x != x) b = 0xffffffffu;
-  return (uint64_t)b << 32 | (0xffffffffu - index);
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-template <class F>
-__device__ __forceinline__ float cta_reduce(float x, float* slot, F f) {
+// Order of logits as an unsigned integer: larger logits larger, a NaN above
+// every number, -0 as +0.
+__device__ __forceinline__ uint32_t rank_bits(float x) {
+  uint32_t b = __float_as_uint(x + 0.f);
+  b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return x != x ? 0xffffffffu : b;
+}
+__device__ __forceinline__ float rank_value(uint32_t b) {
+  return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
+}
+// Total order of (logit, index): among equals the lower index is larger.
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
+  return (uint64_t)rank_bits(x) << 32 | (0xffffffffu - index);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xffffffffu - (uint32_t)k; }
+
+template <class V, class F>
+__device__ __forceinline__ V cta_reduce(V x, V* slot, F f) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
   __syncthreads();
@@ -48,64 +83,369 @@ __device__ __forceinline__ float cta_reduce(float x, float* slot, F f) {
   return x;
 }
 
-// One CTA per row.
+// Largest and smallest of eight values (the largest NaN if one is).
+__device__ __forceinline__ void extremes(const Raw8<bf16>& r, float& hi, float& lo) {
+  const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&r.v);
+  const __nv_bfloat162 a = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  const __nv_bfloat162 b = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+  hi = max_nan(__low2float(a), __high2float(a));
+  lo = fminf(__low2float(b), __high2float(b));
+}
+__device__ __forceinline__ void extremes(const Raw8<fp16>& r, float& hi, float& lo) {
+  const __half2* v = reinterpret_cast<const __half2*>(&r.v);
+  const __half2 a = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  const __half2 b = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+  hi = max_nan(__low2float(a), __high2float(a));
+  lo = fminf(__low2float(b), __high2float(b));
+}
+__device__ __forceinline__ void extremes(const Raw8<float>& r, float& hi, float& lo) {
+  float f[8];
+  widen8<float>(r, f);
+  hi = lo = f[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    hi = max_nan(hi, f[i]);
+    lo = fminf(lo, f[i]);
+  }
+}
+
+// Two fp32 lanes in one instruction (sm_100 and later).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float lane0(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float lane1(uint64_t x) {
+  return __uint_as_float((uint32_t)(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Logits of at least this magnitude are left out of the running softmax (below
+// it they weigh nothing unless the whole row is there); a row whose largest
+// logit is that far out is done again from differences to the maximum.
+constexpr float kFarLogit = 1e30f;
+
+// The running softmax of one thread, in powers of two.  Every term is
+//   e = 2^(x c - ref),  c = inv_temp log2(e),
+// with ref a whole number: x c - ref is one fused multiply-add, and the final
+// log-sum takes ref off exactly (fma(max, c, -ref)), so no error in proportion
+// to the logits' size enters.  ref is set by the first vector and moved only
+// when a term would pass 2^kSlack (sums stay below 2^127), so the loop hardly
+// ever rescales.
+struct Running {
+  static constexpr float kSlack = 64.f;
+  float max = -INFINITY, ref = -INFINITY;
+  uint64_t sum = 0, ent = 0;  // two lanes each; ent: sum of e * (x c - ref)
+
+  __device__ __forceinline__ void move(float hi, float c) {
+    const float to = ceilf(hi * c);
+    const float s = lane0(sum) + lane1(sum), t = lane0(ent) + lane1(ent);
+    if (s > 0.f) {
+      const float f = exp2_approx(ref - to);
+      sum = pair(s * f, 0.f);
+      ent = pair(f * fmaf(ref - to, s, t), 0.f);
+    }
+    ref = to;
+  }
+
+  __device__ __forceinline__ void one(float x, float c) {
+    max = max_nan(max, x);
+    if (x < -kFarLogit) return;
+    if (x * c > ref + kSlack || ref == -INFINITY) move(x, c);
+    const float s = fmaf(x, c, -ref), e = exp2_approx(s);
+    sum = add2(sum, pair(e, 0.f));
+    ent = fma2(pair(e, 0.f), pair(s, 0.f), ent);
+  }
+
+  template <class T>
+  __device__ __forceinline__ void eight(const Raw8<T>& r, float c) {
+    float hi, lo;
+    extremes(r, hi, lo);
+    float f[8];
+    widen8<T>(r, f);
+    if (!(hi * c <= ref + kSlack) || lo < -kFarLogit) {
+      if (lo < -kFarLogit) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {  // f[i] without indexing registers
+          float x = f[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) x = i == j ? f[j] : x;
+          one(x, c);
+        }
+        return;
+      }
+      if (hi == hi) move(hi, c);  // a NaN poisons the sums by itself
+    }
+    max = max_nan(max, hi);
+    const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t s = fma2(pair(f[i], f[i + 1]), c2, r2);
+      const uint64_t e = pair(exp2_approx(lane0(s)), exp2_approx(lane1(s)));
+      sum = add2(sum, e);
+      ent = fma2(e, s, ent);
+    }
+  }
+};
+
+// (max, ref, sum, ent) of two disjoint sets, brought to the larger ref.
+__device__ __forceinline__ TokPartial merge(const TokPartial& a, const TokPartial& b) {
+  TokPartial r;
+  r.max = max_nan(a.max, b.max);
+  r.ref = fmaxf(a.ref, b.ref);
+  r.sum = r.ent = 0.f;
+  // a set without terms has ref = -Inf; a NaN sum is kept
+  if (a.sum != 0.f) {
+    const float d = a.ref - r.ref, f = exp2_approx(d);
+    r.sum += f * a.sum;
+    r.ent += f * fmaf(d, a.sum, a.ent);
+  }
+  if (b.sum != 0.f) {
+    const float d = b.ref - r.ref, f = exp2_approx(d);
+    r.sum += f * b.sum;
+    r.ent += f * fmaf(d, b.sum, b.ent);
+  }
+  return r;
+}
+
+struct TokShared {
+  TokPartial part[kTokWarps];
+  float slot[kTokWarps];
+  uint64_t kslot[kTokWarps];
+  uint32_t group[32];
+  int found;
+  uint64_t cand[1024];
+  uint64_t best[DPOPT_MAX_TOP];
+};
+
+__device__ __forceinline__ TokPartial cta_merge(TokPartial p, TokShared& sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const TokPartial q{__shfl_down_sync(0xffffffffu, p.max, o),
+                       __shfl_down_sync(0xffffffffu, p.ref, o),
+                       __shfl_down_sync(0xffffffffu, p.sum, o),
+                       __shfl_down_sync(0xffffffffu, p.ent, o)};
+    p = merge(p, q);
+  }
+  if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = p;
+  __syncthreads();
+  p = sh.part[0];
+  for (int w = 1; w < kTokWarps; ++w) p = merge(p, sh.part[w]);
+  return p;
+}
+
+// The stretch [lo, hi) of a row as head elements up to a 16-byte boundary,
+// whole 8-element vectors, and a tail.
+template <class T>
+struct Stretch {
+  const T* x;
+  int64_t len, head, vecs;
+  __device__ __forceinline__ Stretch(const T* row, int64_t lo, int64_t hi)
+      : x(row + lo), len(hi > lo ? hi - lo : 0) {
+    const int64_t off = (16 - ((uintptr_t)x & 15)) % 16 / sizeof(T);
+    head = off < len ? off : len;
+    vecs = (len - head) / 8;
+  }
+  // element outside the vectors, t = 0 .. loose() - 1
+  __device__ __forceinline__ int64_t loose() const { return len - vecs * 8; }
+  __device__ __forceinline__ int64_t loose_at(int64_t t) const {
+    return t < head ? t : t + vecs * 8;
+  }
+};
+
+// K = 1 .. top largest of the keys a thread can list, by `top` passes over
+// them: each pass takes the largest below the last.  The form for rows whose
+// candidates are too many for the list (few distinct or few unmasked logits)
+// and for joining the parts' lists.
+template <class F>
+__device__ __forceinline__ void top_by_passes(int top, uint64_t* best, TokShared& sh, F each) {
+  uint64_t last = ~0ull;
+  for (int k = 0; k < top; ++k) {
+    uint64_t b = 0;
+    each([&](uint64_t key) {
+      if (key < last && key > b) b = key;
+    });
+    last = cta_reduce(b, sh.kslot, [](uint64_t a, uint64_t c) { return a > c ? a : c; });
+    if (threadIdx.x == 0) best[k] = last;
+  }
+  __syncthreads();
+}
+
+// The `top` largest keys of a stretch, into sh.best (zeros where it has fewer).
+// thread_max is the largest logit this thread saw: the top-th largest of the
+// 32 maxima over eight threads each is a floor that at least `top` elements
+// reach, and only threads whose own maximum reaches it look at their elements
+// again (about `top` threads of the 256).
+template <class T>
+__device__ void stretch_top(const Stretch<T>& st, int64_t lo, int top, float thread_max,
+                            TokShared& sh) {
+  const uint32_t mine = rank_bits(thread_max);
+  uint32_t g = mine;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if ((threadIdx.x & 7) == 0) sh.group[threadIdx.x >> 3] = g;
+  if (threadIdx.x == 0) sh.found = 0;
+  __syncthreads();
+  g = sh.group[threadIdx.x & 31];
+  int rank = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t o = __shfl_sync(0xffffffffu, g, j);
+    rank += o > g || (o == g && j < (int)(threadIdx.x & 31));
+  }
+  const uint32_t at = __ballot_sync(0xffffffffu, rank == top - 1);
+  const uint32_t floor = __shfl_sync(0xffffffffu, g, __ffs(at) - 1);
+  auto offer = [&](float x, int64_t i) {
+    if (rank_bits(x) < floor) return;
+    const int n = atomicAdd(&sh.found, 1);  // the order in the list does not matter
+    if (n < (int)(sizeof(sh.cand) / 8)) sh.cand[n] = rank_key(x, (uint32_t)(lo + i));
+  };
+  if (mine >= floor) {
+    for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads)
+      offer(to_f32(st.x[st.loose_at(t)]), st.loose_at(t));
+    for (int64_t v = threadIdx.x; v < st.vecs; v += kTokThreads) {
+      float f[8];
+      widen8<T>(ld_raw8<T>(st.x + st.head + v * 8), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) offer(f[i], st.head + v * 8 + i);
+    }
+  }
+  __syncthreads();
+  const int n = sh.found;
+  if (n <= (int)(sizeof(sh.cand) / 8)) {
+    // a candidate's place is the number of larger ones (keys are distinct)
+    for (int i = threadIdx.x; i < top; i += kTokThreads)
+      if (i >= n) sh.best[i] = 0;
+    for (int i = threadIdx.x; i < n; i += kTokThreads) {
+      const uint64_t k = sh.cand[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += sh.cand[j] > k;
+      if (above < top) sh.best[above] = k;
+    }
+    __syncthreads();
+  } else {
+    top_by_passes(top, sh.best, sh, [&](auto take) {
+      for (int64_t j = threadIdx.x; j < st.len; j += kTokThreads)
+        take(rank_key(to_f32(st.x[j]), (uint32_t)(lo + j)));
+    });
+  }
+}
+
+// A row's results from its softmax and its largest keys.
+template <class T>
+__device__ void finish_row(const LogprobParams& p, int64_t row, const T* x, TokPartial t,
+                           const uint64_t* best, TokShared& sh) {
+  const float m = t.max;
+  float logsum = 0.f, shift = 0.f;  // shift: sum of p * (x - m) * inv_temp
+  const bool empty = m == -INFINITY;
+  if (!empty && !(fabsf(m) <= kFarLogit)) {
+    // from differences to the maximum, which do not overflow
+    float sum = 0.f, ent = 0.f;
+    for (int64_t j = threadIdx.x; j < p.vocab; j += kTokThreads) {
+      const float s = (to_f32(x[j]) - m) * p.inv_temp, e = expf(s);
+      sum += e;
+      if (s != -INFINITY) ent = fmaf(e, s, ent);
+    }
+    auto add = [](float a, float b) { return a + b; };
+    sum = cta_reduce(sum, sh.slot, add);
+    ent = cta_reduce(ent, sh.slot, add);
+    logsum = logf(sum);
+    shift = ent / sum;
+  } else if (!empty) {
+    constexpr float kLn2 = 0.693147180559945309f;
+    const float d = fmaf(m, p.c, -t.ref);  // the maximum's own exponent
+    logsum = fmaf(-kLn2, d, logf(t.sum));
+    shift = kLn2 * (t.ent / t.sum - d);
+  }
+  auto logp = [&](float v) { return empty ? -INFINITY : (v - m) * p.inv_temp - logsum; };
+  if (threadIdx.x == 0) {
+    p.stats[row * 2] = m;
+    p.stats[row * 2 + 1] = logsum;
+    if (p.entropy) p.entropy[row] = empty ? 0.f : logsum - shift;
+  }
+  if ((int)threadIdx.x < p.n_tokens) {
+    const int64_t tok = p.tokens[row * p.n_tokens + threadIdx.x];
+    p.logprob[row * p.n_tokens + threadIdx.x] =
+        tok < 0 ? 0.f : tok >= p.vocab ? NAN : logp(to_f32(x[tok]));
+  }
+  const int k = (int)threadIdx.x - 64;  // other threads than the tokens'
+  if (k >= 0 && k < p.top) {
+    const uint32_t j = key_index(best[k]);
+    if (dbg_ok(p.dbg, j < p.vocab)) {
+      p.top_index[row * p.top + k] = j;
+      p.top_logprob[row * p.top + k] = logp(rank_value((uint32_t)(best[k] >> 32)));
+    }
+  }
+}
+
+// One CTA per part of a row: one pass with a running softmax per thread, four
+// vectors in flight.
 template <class T>
 __global__ void __launch_bounds__(kTokThreads) token_logprob_kernel(const LogprobParams p) {
   pdl_enter();
-  __shared__ float slot[kTokWarps];
-  __shared__ uint64_t kslot[kTokWarps];
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < p.vocab; j += kTokThreads) m = max_nan(m, to_f32(x[j]));
-    m = cta_reduce(m, slot, [](float a, float b) { return max_nan(a, b); });
-    float sum = 0.f, ent = 0.f;
-    const bool empty = m == -INFINITY;
-    if (!empty) {
-      for (int64_t j = threadIdx.x; j < p.vocab; j += kTokThreads) {
-        const float s = (to_f32(x[j]) - m) * p.inv_temp;
-        const float e = expf(s);
-        sum += e;
-        if (s != -INFINITY) ent = fmaf(e, s, ent);
-      }
-    }
-    auto add = [](float a, float b) { return a + b; };
-    sum = cta_reduce(sum, slot, add);
-    ent = cta_reduce(ent, slot, add);
-    const float logsum = empty ? 0.f : logf(sum);
-    auto logp = [&](float v) {
-      return empty ? -INFINITY : (v - m) * p.inv_temp - logsum;
-    };
-    if (threadIdx.x == 0) {
-      p.stats[row * 2] = m;
-      p.stats[row * 2 + 1] = logsum;
-      if (p.entropy) p.entropy[row] = empty ? 0.f : logsum - ent / sum;
-    }
-    if ((int)threadIdx.x < p.n_tokens) {
-      const int64_t tok = p.tokens[row * p.n_tokens + threadIdx.x];
-      p.logprob[row * p.n_tokens + threadIdx.x] =
-          tok < 0 ? 0.f : tok >= p.vocab ? NAN : logp(to_f32(x[tok]));
-    }
-    uint64_t last = ~0ull;
-    for (int k = 0; k < p.top; ++k) {
-      uint64_t best = 0;
-      for (int64_t j = threadIdx.x; j < p.vocab; j += kTokThreads) {
-        const uint64_t key = rank_key(to_f32(x[j]), (uint32_t)j);
-        if (key < last && key > best) best = key;
-      }
-      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-      __syncthreads();
-      if ((threadIdx.x & 31) == 0) kslot[threadIdx.x >> 5] = best;
-      __syncthreads();
-      for (int w = 0; w < kTokWarps; ++w) best = max(best, kslot[w]);
-      last = best;
-      const uint32_t j = 0xffffffffu - (uint32_t)best;
-      if (threadIdx.x == 0 && dbg_ok(p.dbg, j < p.vocab)) {
-        p.top_index[row * p.top + k] = j;
-        p.top_logprob[row * p.top + k] = logp(to_f32(x[j]));
-      }
-    }
+  __shared__ TokShared sh;
+  const int64_t row = blockIdx.x / p.parts;
+  const int part = (int)(blockIdx.x - row * p.parts);
+  const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+  const int64_t lo = part * p.part_len;
+  const int64_t hi = min(p.vocab, lo + p.part_len);
+  const Stretch<T> st(x, lo, hi);
+  const T* body = st.x + st.head;
+  Running run;
+  for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads)
+    run.one(to_f32(st.x[st.loose_at(t)]), p.c);
+  int64_t v = threadIdx.x;
+  for (; v + 3 * kTokThreads < st.vecs; v += 4 * kTokThreads) {
+    Raw8<T> r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = ld_raw8<T>(body + (v + u * kTokThreads) * 8);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) run.eight<T>(r[u], p.c);
   }
+  for (; v < st.vecs; v += kTokThreads) run.eight<T>(ld_raw8<T>(body + v * 8), p.c);
+  const TokPartial t = cta_merge(
+      TokPartial{run.max, run.ref, lane0(run.sum) + lane1(run.sum), lane0(run.ent) + lane1(run.ent)},
+      sh);
+  if (p.top > 0) stretch_top<T>(st, lo, p.top, run.max, sh);
+  if (p.parts == 1) {
+    finish_row<T>(p, row, x, t, sh.best, sh);
+    return;
+  }
+  const int64_t at = row * p.parts + part;
+  if (threadIdx.x == 0) p.partial[at] = t;
+  if ((int)threadIdx.x < p.top) p.keys[at * p.top + threadIdx.x] = sh.best[threadIdx.x];
+}
+
+// Joins the parts of a row, one CTA per row.
+template <class T>
+__global__ void __launch_bounds__(kTokThreads) token_logprob_join_kernel(const LogprobParams p) {
+  pdl_enter();
+  __shared__ TokShared sh;
+  __shared__ uint64_t keys[kTokMaxParts * DPOPT_MAX_TOP];
+  const int64_t row = blockIdx.x;
+  const int n = p.parts * p.top;
+  for (int i = threadIdx.x; i < n; i += kTokThreads) keys[i] = p.keys[row * n + i];
+  TokPartial t{-INFINITY, -INFINITY, 0.f, 0.f};
+  if ((int)threadIdx.x < p.parts) t = p.partial[row * p.parts + threadIdx.x];
+  t = cta_merge(t, sh);
+  if (p.top > 0)
+    top_by_passes(p.top, sh.best, sh, [&](auto take) {
+      for (int i = threadIdx.x; i < n; i += kTokThreads) take(keys[i]);
+    });
+  finish_row<T>(p, row, static_cast<const T*>(p.logits) + row * p.ld, t, sh.best, sh);
 }
 
 struct LogprobGradParams {
@@ -114,15 +454,24 @@ struct LogprobGradParams {
   const int64_t* tokens;
   int n_tokens;
   float inv_temp;
+  float c;  // inv_temp * log2(e)
+  int64_t stretches, stretch_len;
   const float *stats, *dlogprob, *entropy, *dentropy;
   const LossScaleState* loss_scale;
   void* dlogits;
   Dbg dbg;
 };
 
-// One CTA per row.  Every element gets its share of -p_j; after a barrier the
-// given tokens' elements, whose logits were read before (dlogits may be the
-// logits), are stored again with their own terms.
+// A row is cut into stretches of kGradStretch elements, one CTA each.  Every
+// element gets its share of -p_j; after a barrier the given tokens' elements of
+// the stretch, whose logits were read before (dlogits may be the logits), are
+// stored again with their own terms.  With
+//   q = (x - m) c - L log2(e)   (the log probability in powers of two)
+// an element is 2^q (A + B q): A = -scale (sum dlogprob + dentropy entropy), B =
+// -scale dentropy ln 2.  q is held above -1e4, where 2^q is 0 in fp32: a masked
+// entry gives 0 and no product overflows.
+constexpr int64_t kGradStretch = 4 * kTokThreads * 8;
+
 template <class T>
 __global__ void __launch_bounds__(kTokThreads)
 token_logprob_grad_kernel(const LogprobGradParams p) {
@@ -130,46 +479,101 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
   __shared__ int64_t tok[DPOPT_MAX_TOKENS];
   __shared__ float dlp[DPOPT_MAX_TOKENS];
   __shared__ T given[DPOPT_MAX_TOKENS];
+  const int64_t row = blockIdx.x / p.stretches;
+  const int64_t lo = (blockIdx.x - row * p.stretches) * p.stretch_len;
+  const int64_t hi = min(p.vocab, lo + p.stretch_len);
+  const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+  T* out = static_cast<T*>(p.dlogits) + row * p.ld_out;
   const float scale = (p.loss_scale ? p.loss_scale->scale : 1.f) * p.inv_temp;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-    T* out = static_cast<T*>(p.dlogits) + row * p.ld_out;
-    __syncthreads();
-    if ((int)threadIdx.x < p.n_tokens) {
-      const int64_t t = p.tokens[row * p.n_tokens + threadIdx.x];
-      tok[threadIdx.x] = t;
-      dlp[threadIdx.x] = t < 0 ? 0.f : t >= p.vocab ? NAN : p.dlogprob[row * p.n_tokens + threadIdx.x];
-      if (t >= 0 && t < p.vocab) given[threadIdx.x] = x[t];
+  const float m = p.stats[row * 2], logsum = p.stats[row * 2 + 1];
+  const float dh = p.dentropy ? p.dentropy[row] : 0.f;
+  const float ent = p.dentropy ? p.entropy[row] : 0.f;
+  if ((int)threadIdx.x < p.n_tokens) {
+    const int64_t t = p.tokens[row * p.n_tokens + threadIdx.x];
+    tok[threadIdx.x] = t;
+    dlp[threadIdx.x] =
+        t < 0 ? 0.f : t >= p.vocab ? NAN : p.dlogprob[row * p.n_tokens + threadIdx.x];
+    if (t >= lo && t < hi) given[threadIdx.x] = x[t];
+  }
+  __syncthreads();
+  float a = 0.f;
+  bool none = true;  // no token given
+  for (int i = 0; i < p.n_tokens; ++i) {
+    a += dlp[i];
+    none = none && tok[i] < 0;
+  }
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  const bool zero = m == -INFINITY || (none && dh == 0.f);
+  const float l2 = logsum * kLog2e;
+  const float A = -scale * fmaf(dh, ent, a), B = -scale * dh * kLn2;
+  const Stretch<T> st(x, lo, hi);
+  T* dst = out + lo;
+  auto grad = [&](float v) {
+    const float q = max_nan(fmaf(v - m, p.c, -l2), -1e4f);
+    return zero ? 0.f : exp2_approx(q) * fmaf(B, q, A);
+  };
+  for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads) {
+    const int64_t j = st.loose_at(t);
+    dst[j] = from_f32<T>(grad(to_f32(st.x[j])));
+  }
+  const bool vec = ((uintptr_t)(dst + st.head) & 15) == 0;
+  const T* body = st.x + st.head;
+  auto eight = [&](const Raw8<T>& r, int64_t v) {
+    float f[8];
+    widen8<T>(r, f);
+    const uint64_t c2 = pair(p.c, p.c), m2 = pair(-m, -m), l22 = pair(-l2, -l2);
+    const uint64_t A2 = pair(A, A), B2 = pair(B, B);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      uint64_t q = fma2(add2(pair(f[i], f[i + 1]), m2), c2, l22);
+      q = pair(max_nan(lane0(q), -1e4f), max_nan(lane1(q), -1e4f));
+      q = mul2(pair(exp2_approx(lane0(q)), exp2_approx(lane1(q))), fma2(B2, q, A2));
+      f[i] = lane0(q);
+      f[i + 1] = lane1(q);
     }
-    __syncthreads();
-    float a = 0.f;
-    for (int i = 0; i < p.n_tokens; ++i) a += dlp[i];
-    const float m = p.stats[row * 2], logsum = p.stats[row * 2 + 1];
-    const float dh = p.dentropy ? p.dentropy[row] : 0.f;
-    const float ent = p.dentropy ? p.entropy[row] : 0.f;
-    const bool empty = m == -INFINITY;
-    // the gradient of one logit whose own tokens add `own`
-    auto grad = [&](float v, float own) {
-      const float lp = (v - m) * p.inv_temp - logsum;
-      const float e = expf(lp);
-      if (empty || v == -INFINITY) return 0.f;
-      // e = 0: lp may be so large that its product with dh overflows, or overflow itself
-      return scale * (own - (e == 0.f ? 0.f : e * fmaf(dh, lp + ent, a)));
-    };
-    for (int64_t j = threadIdx.x; j < p.vocab; j += kTokThreads)
-      out[j] = from_f32<T>(grad(to_f32(x[j]), 0.f));
-    __syncthreads();
-    if ((int)threadIdx.x < p.n_tokens) {
-      const int64_t t = tok[threadIdx.x];
-      bool mine = t >= 0 && t < p.vocab;
-      float own = 0.f;
-      for (int i = 0; i < p.n_tokens; ++i)
-        if (tok[i] == t) {
-          if (i < (int)threadIdx.x) mine = false;  // an equal token before this one stores it
-          own += dlp[i];
-        }
-      if (mine && dbg_ok(p.dbg, t < p.vocab))
-        out[t] = from_f32<T>(grad(to_f32(given[threadIdx.x]), own));
+    T* d = dst + st.head + v * 8;
+    if (vec) {
+      st_vec8<T>(d, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = from_f32<T>(f[i]);
+    }
+  };
+  if (zero) {  // nothing to read
+    float f[8] = {};
+    for (int64_t v = threadIdx.x; v < st.vecs; v += kTokThreads) {
+      T* d = dst + st.head + v * 8;
+      if (vec) {
+        st_vec8<T>(d, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = from_f32<T>(0.f);
+      }
+    }
+    return;
+  }
+  int64_t v = threadIdx.x;
+  for (; v + 3 * kTokThreads < st.vecs; v += 4 * kTokThreads) {
+    Raw8<T> r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = ld_raw8<T>(body + (v + u * kTokThreads) * 8);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) eight(r[u], v + u * kTokThreads);
+  }
+  for (; v < st.vecs; v += kTokThreads) eight(ld_raw8<T>(body + v * 8), v);
+  __syncthreads();
+  if ((int)threadIdx.x < p.n_tokens) {
+    const int64_t t = tok[threadIdx.x];
+    bool mine = t >= lo && t < hi;
+    float own = 0.f;
+    for (int i = 0; i < p.n_tokens; ++i)
+      if (tok[i] == t) {
+        if (i < (int)threadIdx.x) mine = false;  // an equal token before this one stores it
+        own += dlp[i];
+      }
+    if (mine && dbg_ok(p.dbg, t < p.vocab)) {
+      const float v = to_f32(given[threadIdx.x]);
+      out[t] = from_f32<T>(v == -INFINITY ? 0.f : fmaf(scale, own, grad(v)));
     }
   }
 }
@@ -186,6 +590,17 @@ int check_logits(int dtype, int64_t rows, int64_t vocab, int n_tokens, float inv
   return DPOPT_OK;
 }
 
+// inv_temperature * log2(e), rounded once.
+float log2_scale(float inv_temperature) {
+  return (float)((double)inv_temperature * 1.4426950408889634074);
+}
+
+// Length of one of `parts` stretches of a row: whole vectors, so that a row that
+// starts on a 16-byte boundary is cut on such boundaries.
+int64_t part_length(int64_t vocab, int64_t parts) {
+  return ((vocab + parts - 1) / parts + 7) / 8 * 8;
+}
+
 }  // namespace
 }  // namespace dpopt
 
@@ -198,7 +613,8 @@ int dpopt_token_logprob_scratch_bytes(int64_t rows, int64_t vocab, int top, int6
   DPOPT_TRY(check_logits(DPOPT_GRAD_F32, rows, vocab, 0, 1.f));
   if (top < 0 || top > DPOPT_MAX_TOP || top > vocab)
     return fail(DPOPT_ERR_INVALID_ARG, "top must lie in [0, min(vocab, %d)]", DPOPT_MAX_TOP);
-  *bytes_out = 0;
+  const int64_t parts = tok_parts(rows, vocab);
+  *bytes_out = parts == 1 ? 0 : rows * parts * (int64_t)(sizeof(TokPartial) + 8 * top);
   return DPOPT_OK;
 }
 
@@ -239,16 +655,39 @@ int dpopt_token_logprob(const void* logits, int dtype, int64_t rows, int64_t voc
     DPOPT_TRY(take_matrix("scratch", dpopt_matrix{scratch, need}, 1, need, 1, true, &dummy, s, &n));
   }
   DPOPT_TRY(check_overlaps(s, n));
-  LogprobParams p{rows,     vocab, x.ld,    logits,  tokens,      n_tokens,  top,
-                  inv_temperature, logprob, stats,   entropy,     top_logprob, top_index, make_dbg()};
-  int sms = 0;
-  DPOPT_TRY(sm_count(&sms));
+  LogprobParams p{};
+  p.rows = rows;
+  p.vocab = vocab;
+  p.ld = x.ld;
+  p.logits = logits;
+  p.tokens = tokens;
+  p.n_tokens = n_tokens;
+  p.top = top;
+  p.inv_temp = inv_temperature;
+  p.c = log2_scale(inv_temperature);
+  p.parts = (int)tok_parts(rows, vocab);
+  p.part_len = part_length(vocab, p.parts);
+  p.logprob = logprob;
+  p.stats = stats;
+  p.entropy = entropy;
+  p.top_logprob = top_logprob;
+  p.top_index = top_index;
+  p.partial = static_cast<TokPartial*>(scratch);
+  p.keys = reinterpret_cast<uint64_t*>(p.partial + rows * p.parts);
+  p.dbg = make_dbg();
+  if (rows * p.parts > INT32_MAX) return fail(DPOPT_ERR_UNSUPPORTED, "too many rows");
   auto kern = dtype == DPOPT_GRAD_BF16  ? token_logprob_kernel<bf16>
               : dtype == DPOPT_GRAD_F16 ? token_logprob_kernel<fp16>
                                         : token_logprob_kernel<float>;
-  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)sms * 8);
-  return launched(launch_pdl(kern, grid, kTokThreads, 0, (cudaStream_t)stream, p),
-                  "token logprob");
+  DPOPT_TRY(launched(launch_pdl(kern, (unsigned)(rows * p.parts), kTokThreads, 0,
+                                (cudaStream_t)stream, p),
+                     "token logprob"));
+  if (p.parts == 1) return DPOPT_OK;
+  auto join = dtype == DPOPT_GRAD_BF16  ? token_logprob_join_kernel<bf16>
+              : dtype == DPOPT_GRAD_F16 ? token_logprob_join_kernel<fp16>
+                                        : token_logprob_join_kernel<float>;
+  return launched(launch_pdl(join, (unsigned)rows, kTokThreads, 0, (cudaStream_t)stream, p),
+                  "token logprob join");
 }
 
 int dpopt_token_logprob_backward(const void* logits, int dtype, int64_t rows, int64_t vocab,
@@ -290,17 +729,31 @@ int dpopt_token_logprob_backward(const void* logits, int dtype, int64_t rows, in
                           dpopt_matrix{const_cast<dpopt_loss_scale_state*>(loss_scale), 32}, 1,
                           sizeof(dpopt_loss_scale_state), 1, false, &dummy, s, &n));
   DPOPT_TRY(check_overlaps(s, n));
-  LogprobGradParams p{rows,  vocab,    x.ld,    d.ld,     logits,
-                      tokens, n_tokens, inv_temperature, stats, dlogprob,
-                      entropy, dentropy, reinterpret_cast<const LossScaleState*>(loss_scale),
-                      dlogits, make_dbg()};
-  int sms = 0;
-  DPOPT_TRY(sm_count(&sms));
+  LogprobGradParams p{};
+  p.rows = rows;
+  p.vocab = vocab;
+  p.ld = x.ld;
+  p.ld_out = d.ld;
+  p.logits = logits;
+  p.tokens = tokens;
+  p.n_tokens = n_tokens;
+  p.inv_temp = inv_temperature;
+  p.c = log2_scale(inv_temperature);
+  p.stretches = (vocab + kGradStretch - 1) / kGradStretch;
+  p.stretch_len = part_length(vocab, p.stretches);
+  p.stats = stats;
+  p.dlogprob = dlogprob;
+  p.entropy = entropy;
+  p.dentropy = dentropy;
+  p.loss_scale = reinterpret_cast<const LossScaleState*>(loss_scale);
+  p.dlogits = dlogits;
+  p.dbg = make_dbg();
+  if (rows > INT32_MAX / p.stretches) return fail(DPOPT_ERR_UNSUPPORTED, "too many rows");
   auto kern = dtype == DPOPT_GRAD_BF16  ? token_logprob_grad_kernel<bf16>
               : dtype == DPOPT_GRAD_F16 ? token_logprob_grad_kernel<fp16>
                                         : token_logprob_grad_kernel<float>;
-  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)sms * 8);
-  return launched(launch_pdl(kern, grid, kTokThreads, 0, (cudaStream_t)stream, p),
+  return launched(launch_pdl(kern, (unsigned)(rows * p.stretches), kTokThreads, 0,
+                             (cudaStream_t)stream, p),
                   "token logprob gradient");
 }
 
