@@ -8,12 +8,17 @@
 namespace dpopt {
 namespace {
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
+// A row is held by a group of tpr threads (a multiple of 32), in NV fragments of 8
+// columns per thread: as few as 512 threads can cover the row with.  In the vector form (VEC: every matrix may be
+// moved 16 bytes at a time) thread t's fragment v is the columns
+// (v tpr + t) 8 .. + 7; in the element form, for odd widths and alignments, its
+// element i is column (v 8 + i) tpr + t, so that a warp always touches
+// neighbouring columns.  Either way a block of 32 columns lies in one warp.
+constexpr int kJoinCta = 512, kJoinSms = 152;
 
 struct JoinParams {
   int64_t rows, cols;
-  int64_t groups;  // 8-column groups of a row, rounded up to whole 32-column blocks
+  int tpr, groups;  // threads of a row, rows at a time in a CTA
   int param_dtype;
   float eps, res_scale, branch_scale;
   int64_t gate_rows;
@@ -24,30 +29,118 @@ struct JoinParams {
   Dbg dbg;
 };
 
-// Sum over the CTA of N values at once, the same bits in every thread: each
-// warp's butterfly, then the warps' sums in warp order.
+__host__ __device__ inline int row_frags(int64_t cols) { return cols <= 8 * kJoinCta ? 1 : cols <= 16 * kJoinCta ? 2 : 4; }
+__host__ __device__ inline int row_threads(int64_t cols) {
+  const int64_t per_warp = 256 * row_frags(cols);
+  return (int)((cols + per_warp - 1) / per_warp) * 32;
+}
+
+template <bool VEC>
+__device__ __forceinline__ int column(int v, int i, int t, int tpr) {
+  return VEC ? (v * tpr + t) * 8 + i : (v * 8 + i) * tpr + t;
+}
+
+// Barrier of one row's threads (a whole number of warps).
+__device__ __forceinline__ void group_sync(int group, int tpr) {
+  if (tpr == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+}
+
+// Sum of N values over a row's threads, the same bits in each: the warps'
+// butterflies, then the warps' sums in warp order.  `slot` has a place per warp
+// of the CTA; callers alternate between two such arrays, so that one barrier is
+// enough.
 template <int N>
-__device__ __forceinline__ void cta_sum(float (&x)[N], float (*slot)[N]) {
-  const int warp = threadIdx.x >> 5;
+__device__ __forceinline__ void group_sum(float (&x)[N], float (*slot)[N], int group, int tpr) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
-  __syncthreads();  // the slots' earlier readers are done
-  if ((threadIdx.x & 31) == 0)
+  if (tpr == 32) return;
+  const int warps = tpr >> 5, first = group * warps, lane = threadIdx.x & 31;
+  if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[warp][i] = x[i];
-  __syncthreads();
+    for (int i = 0; i < N; ++i) slot[threadIdx.x >> 5][i] = x[i];
+  group_sync(group, tpr);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    x[i] = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x[i] += slot[w][i];
+    if (warps <= 4) {
+      x[i] = slot[first][i];
+      for (int w = 1; w < warps; ++w) x[i] += slot[first + w][i];
+    } else {
+      x[i] = warp_sum(lane < warps ? slot[first + lane][i] : 0.f);
+    }
   }
 }
 
-// Eight values of a weight, or ones.
-__device__ __forceinline__ void weight8(const void* w, int dtype, int64_t col, int64_t cols,
-                                        float (&f)[8]) {
+// One fragment of a matrix in the type it is stored in.
+template <class T, bool VEC>
+struct Frag;
+template <class T>
+struct Frag<T, true> {
+  Raw8<T> r;
+  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
+                                       int64_t cols) {
+    const int c = column<true>(v, 0, t, tpr);
+    r = Raw8<T>{};
+    if (c < cols) r = ld_raw8<T>(static_cast<const T*>(m.data) + row * m.ld + c);
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const { widen8<T>(r, f); }
+};
+template <class T>
+struct Frag<T, false> {
+  T e[8];
+  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
+                                       int64_t cols) {
+    const T* p = static_cast<const T*>(m.data) + row * m.ld;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = w && col + i < cols ? ld_any(w, dtype, col + i) : 1.f;
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<false>(v, i, t, tpr);
+      e[i] = c < cols ? p[c] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
+  }
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void frag_store(const Mat& m, int64_t row, int v, int t, int tpr,
+                                           int64_t cols, const float (&f)[8]) {
+  T* p = static_cast<T*>(m.data) + row * m.ld;
+  if constexpr (VEC) {
+    const int c = column<true>(v, 0, t, tpr);
+    if (c < cols) st_vec8<T>(p + c, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<false>(v, i, t, tpr);
+      if (c < cols) p[c] = from_f32<T>(f[i]);
+    }
+  }
+}
+
+// Pack a fragment: in the vector form four threads share a block, in the element
+// form a warp's 32 neighbouring columns are one.  Whole warps call it.
+template <class T, bool VEC>
+__device__ __forceinline__ void frag_pack(const Act8Out& o, int64_t row, int v, int t, int tpr,
+                                          int64_t cols, const float (&f)[8]) {
+  if constexpr (VEC) {
+    act8_store8<T>(o, row, column<true>(v, 0, t, tpr), cols, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<false>(v, i, t, tpr);
+      const uint32_t amax =
+          __reduce_max_sync(0xffffffffu, __float_as_uint(f[i]) & 0x7fffffffu);
+      const uint32_t byte = act8_byte<T>(amax);
+      if (c < cols) {
+        o.codes[row * o.ld_codes + c] = (int8_t)act8_code(f[i], act8_inverse(byte));
+        if ((t & 31) == 0) o.exps[row * o.ld_exps + c / kAct8Block] = (uint8_t)byte;
+      }
+    }
+  }
 }
 
 template <class T>
@@ -56,78 +149,130 @@ __device__ __forceinline__ void round8(const float (&f)[8], float (&r)[8]) {
   for (int i = 0; i < 8; ++i) r[i] = to_f32(from_f32<T>(f[i]));
 }
 
+// Values of a parameter (row `at` elements in; ones where it is absent) at a
+// thread's columns, into its places out[i * stride].  Not inlined: parameters are
+// read once per launch or gate row, and their three types and eight addresses
+// would take the registers of the loops around it.
+template <bool VEC, int NV>
+__device__ __noinline__ void stage_param(const void* w, int dtype, int64_t at, int t, int tpr,
+                                         int64_t cols, float* out, int stride) {
+#pragma unroll 1
+  for (int v = 0; v < NV; ++v)
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<VEC>(v, i, t, tpr);
+      out[(v * 8 + i) * stride] = w && c < cols ? ld_any(w, dtype, at + c) : 1.f;
+    }
+}
+
 __device__ __forceinline__ int64_t gate_row_of(int64_t gate_rows, int64_t row) {
   return gate_rows > 0 ? row / gate_rows : 0;
 }
 
-// One CTA per row, the fp32 row of h_out in shared memory between the two
-// norms: any width, stride and alignment.
-template <class T>
-__global__ void __launch_bounds__(kJoinThreads) block_join_kernel(const JoinParams p) {
+// A group of threads walks rows; the next row's h and y are loaded before the
+// present row's two sums, and h_out stays in registers in fp32 between the norms.
+// The parameters are kept as branch_scale * gate * w_post and w_pre.
+template <class T, bool VEC, int NV>
+__global__ void __launch_bounds__(kJoinCta, 1)
+    block_join_kernel(const __grid_constant__ JoinParams p) {
   pdl_enter();
-  extern __shared__ float hrow[];  // groups * 8
-  __shared__ float slot[kJoinWarps][1];
-  const int64_t rounds = (p.groups + kJoinThreads - 1) / kJoinThreads;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  __shared__ float slot[2][kJoinCta / 32][1];
+  const int group = threadIdx.x / p.tpr, t = threadIdx.x - group * p.tpr;
+  const int64_t step = (int64_t)gridDim.x * p.groups;
+  int64_t row = (int64_t)blockIdx.x * p.groups + group;
+  const float inv_c = 1.f / (float)p.cols;
+  int64_t held = -1;  // gate row in pb
+  float pb[NV][8], wpre[NV][8];
+  extern __shared__ float stage[];  // 8 NV places per thread
+  float* mine = stage + threadIdx.x;
+  const int stride = blockDim.x;
+  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wpre[v][i] = mine[(v * 8 + i) * stride];
+  Frag<T, VEC> fh[NV], fy[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (row < p.rows) {
+      fh[v].load(p.h, row, v, t, p.tpr, p.cols);
+      fy[v].load(p.y, row, v, t, p.tpr, p.cols);
+    }
+  for (; row < p.rows; row += step) {
+    if (!dbg_ok(p.dbg, row >= 0 && p.tpr * 8 * NV >= p.cols)) break;
+    const int64_t grow = gate_row_of(p.gate_rows, row);
+    if (grow != held) {
+      held = grow;
+      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pb[v][i] = p.branch_scale * mine[(v * 8 + i) * stride];
+      if (p.gate.data) {
+        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, p.tpr, p.cols, mine,
+                             stride);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pb[v][i] *= mine[(v * 8 + i) * stride];
+      }
+    }
+    float h[NV][8], y[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      fh[v].widen(h[v]);
+      fy[v].widen(y[v]);
+      if (row + step < p.rows) {
+        fh[v].load(p.h, row + step, v, t, p.tpr, p.cols);
+        fy[v].load(p.y, row + step, v, t, p.tpr, p.cols);
+      }
+    }
     float rpost = 1.f;
     if (p.rstd_post) {
       float ss[1] = {0.f};
-      for (int64_t g = threadIdx.x; g < p.groups; g += kJoinThreads) {
-        float y[8];
-        mat_load8<T>(p.y, row, g * 8, p.cols, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
-      }
-      cta_sum<1>(ss, slot);
-      rpost = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
-      if (threadIdx.x == 0) p.rstd_post[row] = rpost;
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[v][i], y[v][i], ss[0]);
+      group_sum<1>(ss, slot[0], group, p.tpr);
+      rpost = 1.f / sqrtf(fmaf(ss[0], inv_c, p.eps));
+      if (t == 0) p.rstd_post[row] = rpost;
     }
-    const int64_t grow = gate_row_of(p.gate_rows, row);
     float ss[1] = {0.f};
-    for (int64_t it = 0; it < rounds; ++it) {
-      const int64_t g = it * kJoinThreads + threadIdx.x;
-      const int64_t col = g * 8;  // may lie past the row: zeros, nothing stored
-      float y[8], h[8], w[8], hr[8];
-      mat_load8<T>(p.y, row, col, p.cols, y);
-      mat_load8<T>(p.h, row, col, p.cols, h);
-      weight8(p.w_post, p.param_dtype, col, p.cols, w);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float gate = p.gate.data && col + i < p.cols
-                               ? ld_any(p.gate.data, p.param_dtype, grow * p.gate.ld + col + i)
-                               : 1.f;
-        const float z = y[i] * rpost * w[i];
-        h[i] = p.res_scale * h[i] + p.branch_scale * gate * z;
-        if (col + i < p.cols) ss[0] = fmaf(h[i], h[i], ss[0]);
+        h[v][i] = fmaf(pb[v][i], y[v][i] * rpost, p.res_scale * h[v][i]);
+        ss[0] = fmaf(h[v][i], h[v][i], ss[0]);
       }
-      mat_store8<T>(p.h_out, row, col, p.cols, h);
-      if (p.y8.codes) act8_store8<T>(p.y8, row, col, p.cols, y);
+      frag_store<T, VEC>(p.h_out, row, v, t, p.tpr, p.cols, h[v]);
+      if (p.y8.codes) frag_pack<T, VEC>(p.y8, row, v, t, p.tpr, p.cols, y[v]);
       if (p.h8.codes) {
-        round8<T>(h, hr);
-        act8_store8<T>(p.h8, row, col, p.cols, hr);
-      }
-      if (g < p.groups) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hrow[col + i] = h[i];
+        float r[8];
+        round8<T>(h[v], r);
+        frag_pack<T, VEC>(p.h8, row, v, t, p.tpr, p.cols, r);
       }
     }
-    if (!p.u.data) continue;
-    cta_sum<1>(ss, slot);
-    const float rpre = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
-    if (threadIdx.x == 0) p.rstd_pre[row] = rpre;
-    for (int64_t it = 0; it < rounds; ++it) {
-      const int64_t g = it * kJoinThreads + threadIdx.x;
-      const int64_t col = g * 8;
-      float u[8], w[8], ur[8];
-      weight8(p.w_pre, p.param_dtype, col, p.cols, w);
+    if (!p.u.data) {
+      group_sync(group, p.tpr);  // the slots of the only sum are used again next row
+      continue;
+    }
+    group_sum<1>(ss, slot[1], group, p.tpr);
+    const float rpre = 1.f / sqrtf(fmaf(ss[0], inv_c, p.eps));
+    if (t == 0) p.rstd_pre[row] = rpre;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = col + i < p.cols ? hrow[col + i] * rpre * w[i] : 0.f;
-      mat_store8<T>(p.u, row, col, p.cols, u);
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[v][i] *= rpre * wpre[v][i];
+      frag_store<T, VEC>(p.u, row, v, t, p.tpr, p.cols, h[v]);
       if (p.u8.codes) {
-        round8<T>(u, ur);
-        act8_store8<T>(p.u8, row, col, p.cols, ur);
+        float r[8];
+        round8<T>(h[v], r);
+        frag_pack<T, VEC>(p.u8, row, v, t, p.tpr, p.cols, r);
       }
     }
+    if (!p.rstd_post) group_sync(group, p.tpr);
   }
 }
 
@@ -135,18 +280,25 @@ __global__ void __launch_bounds__(kJoinThreads) block_join_kernel(const JoinPara
 // gradient
 // ---------------------------------------------------------------------------
 
-// Sums over rows: the rows are cut into at most kJoinParts runs, whose number
-// and borders depend on the row count alone.  Each run's CTA leaves one partial
-// row per sum in scratch and the finish kernel adds them in order, so the
-// result does not depend on the GPU or on timing.
-constexpr int kJoinParts = 304;
+// Sums over rows: the rows are cut into runs, whose number and borders depend on
+// the sizes alone (as many as 152 SMs hold groups of threads at a time, but no
+// run of fewer than kPartMinRows rows when there are more rows than SMs).  Each run's
+// group leaves one partial row per sum in scratch and the finish kernel adds them
+// in order, so the result does not depend on the GPU or on timing.
+constexpr int kPartMinRows = 4;
 
-__host__ __device__ inline int64_t part_rows(int64_t rows) {
-  const int64_t parts = rows < kJoinParts ? rows : kJoinParts;
-  return parts == 0 ? 1 : (rows + parts - 1) / parts;
+// Groups of threads a CTA holds at most: a named barrier each.
+__host__ __device__ inline int groups_most(int64_t cols) {
+  const int n = kJoinCta / row_threads(cols);
+  return n < 1 ? 1 : n < 15 ? n : 15;
 }
-__host__ __device__ inline int64_t part_count(int64_t rows) {
-  return (rows + part_rows(rows) - 1) / part_rows(rows);
+__host__ __device__ inline int64_t part_rows(int64_t rows, int64_t cols) {
+  const int64_t at_once = (int64_t)kJoinSms * groups_most(cols);
+  const int64_t each = (rows + at_once - 1) / at_once;
+  return each < kPartMinRows && rows > kJoinSms ? kPartMinRows : each < 1 ? 1 : each;
+}
+__host__ __device__ inline int64_t part_count(int64_t rows, int64_t cols) {
+  return (rows + part_rows(rows, cols) - 1) / part_rows(rows, cols);
 }
 
 // Partial rows of one part: dw_pre, dw_post, and up to two of dgate (of the
@@ -155,7 +307,12 @@ __host__ __device__ inline int64_t part_count(int64_t rows) {
 enum { kPartWPre = 0, kPartWPost = 1, kPartGateFirst = 2, kPartGateLast = 3, kPartSlots = 4 };
 
 struct JoinGradParams {
-  int64_t rows, cols, groups;
+  int64_t rows, cols, width;  // width: cols rounded up to whole blocks
+  int tpr, groups;
+  // the vector form's ring in shared memory: rows held, bytes of one, and where and
+  // how large the fragments of each array are (enum kIn*)
+  int stages;
+  uint32_t stage_bytes, frag_at[4], frag_bytes[4];
   int param_dtype;
   float res_scale, branch_scale;
   int64_t gate_rows;
@@ -164,12 +321,12 @@ struct JoinGradParams {
   const void *w_post, *w_pre;
   const float *rstd_post, *rstd_pre;
   void *dw_post, *dw_pre;
-  float* partial;  // [part][kPartSlots][groups * 8]
+  float* partial;  // [part][kPartSlots][width]
   Dbg dbg;
 };
 
 __device__ __forceinline__ float* part_row(const JoinGradParams& p, int64_t part, int slot) {
-  return p.partial + (part * kPartSlots + slot) * p.groups * 8;
+  return p.partial + (part * kPartSlots + slot) * p.width;
 }
 
 // Rows [lo, hi) that use the gate row of `row`.
@@ -179,116 +336,341 @@ __host__ __device__ inline void gate_span(int64_t gate_rows, int64_t rows, int64
   *hi = gate_rows > 0 && *lo + gate_rows < rows ? *lo + gate_rows : rows;
 }
 
-// One CTA per run of rows.  Per row one pass forms three sums,
-//   s = <w_pre du, h>,  a = <q, dh_out + r1 w_pre du>,  b = <q, h>,
-//   q = w_post gate y,
-// from which <w_post dz, y> = branch (a - r1^3 s / C b); a second pass forms the
-// outputs.  The sums over rows stay in shared memory, each column owned by one
-// thread.
-template <class T>
-__global__ void __launch_bounds__(kJoinThreads) block_join_grad_kernel(const JoinGradParams p) {
-  pdl_enter();
-  extern __shared__ float acc[];  // [3][groups * 8]: dw_pre, dw_post, dgate
-  __shared__ float slot[kJoinWarps][3];
-  const int64_t width = p.groups * 8;
-  const int64_t part = blockIdx.x;
-  const int64_t lo = part * part_rows(p.rows);
-  const int64_t hi = min(p.rows, lo + part_rows(p.rows));
-  const float inv_c = 1.f / (float)p.cols;
-  for (int64_t g = threadIdx.x; g < p.groups; g += kJoinThreads)
-    for (int i = 0; i < 24; ++i) acc[(i >> 3) * width + g * 8 + (i & 7)] = 0.f;
-  bool first_gate = true;
-  for (int64_t row = lo; row < hi; ++row) {
-    const int64_t grow = gate_row_of(p.gate_rows, row);
-    const float r1 = p.du.data ? p.rstd_pre[row] : 0.f;
-    const float r2 = p.rstd_post ? p.rstd_post[row] : 1.f;
-    auto load = [&](int64_t col, float (&d)[8], float (&t)[8], float (&h)[8], float (&y)[8],
-                    float (&wp)[8], float (&g)[8]) {
-      mat_load8<T>(p.dh_out, row, col, p.cols, d);
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The four arrays a gradient row reads, as a thread gets at its fragments.
+// Vector form: a ring of rows in shared memory, each thread copying (cp.async) and
+// reading only its own fragments, so that rows are in flight without registers
+// and without barriers.  Element form: straight from global memory (the second
+// reading of a row comes from L1).
+enum { kInDh = 0, kInDu = 1, kInY = 2, kInH = 3 };
+
+template <class T, bool VEC, int NV>
+struct GradRow {
+  const JoinGradParams& p;
+  int t;
+  uint32_t ring;         // this group's ring
+  float scale[2][NV];    // block scales of y and h of the present row
+  uint32_t next[2][NV];  // and the bytes of the next row's
+
+  __device__ __forceinline__ GradRow(const JoinGradParams& q, int t_, uint32_t r)
+      : p(q), t(t_), ring(r) {}
+
+  __device__ __forceinline__ const Mat& mat(int which) const {
+    return which == kInDh ? p.dh_out : which == kInDu ? p.du : which == kInY ? p.y : p.h_out;
+  }
+  __device__ __forceinline__ const Act8Out& act(int which) const {
+    return which == kInY ? p.y8 : p.h8;
+  }
+  __device__ __forceinline__ bool packed(int which) const {
+    return which == kInY ? p.y8.codes != nullptr : which == kInH && p.h8.codes != nullptr;
+  }
+  __device__ __forceinline__ bool present(int which) const {
+    return which == kInDh || which == kInY || p.du.data != nullptr;
+  }
+  __device__ __forceinline__ uint32_t slot(int stage, int which, int v) const {
+    return ring + stage * p.stage_bytes + p.frag_at[which] + (v * p.tpr + t) * p.frag_bytes[which];
+  }
+
+  // Start the copies of a row.
+  __device__ __forceinline__ void fetch(int64_t row, int stage) {
+    if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = h[i] = 0.f;
-      if (p.du.data) {
-        mat_load8<T>(p.du, row, col, p.cols, t);
-        if (p.h8.codes)
-          act8_load8(p.h8, row, col, p.cols, h);
-        else
-          mat_load8<T>(p.h_out, row, col, p.cols, h);
-      }
-      if (p.y8.codes)
-        act8_load8(p.y8, row, col, p.cols, y);
-      else
-        mat_load8<T>(p.y, row, col, p.cols, y);
-      weight8(p.w_post, p.param_dtype, col, p.cols, wp);
+      for (int which = 0; which < 4; ++which) {
+        if (!present(which)) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        g[i] = p.gate.data && col + i < p.cols
-                   ? ld_any(p.gate.data, p.param_dtype, grow * p.gate.ld + col + i)
-                   : 1.f;
-    };
-    float sum[3] = {0.f, 0.f, 0.f};
-    for (int64_t gi = threadIdx.x; gi < p.groups; gi += kJoinThreads) {
-      const int64_t col = gi * 8;
-      float d[8], t[8], h[8], y[8], wp[8], g[8], w[8];
-      load(col, d, t, h, y, wp, g);
-      weight8(p.w_pre, p.param_dtype, col, p.cols, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (col + i >= p.cols) continue;
-        const float q = wp[i] * g[i] * y[i], wd = w[i] * t[i];
-        sum[0] = fmaf(wd, h[i], sum[0]);
-        sum[1] = fmaf(q, fmaf(r1, wd, d[i]), sum[1]);
-        sum[2] = fmaf(q, h[i], sum[2]);
+        for (int v = 0; v < NV; ++v) {
+          const int c = column<true>(v, 0, t, p.tpr);
+          if (c >= p.cols) continue;
+          if (packed(which)) {
+            copy_async8(slot(stage, which, v), act(which).codes + row * act(which).ld_codes + c);
+          } else {
+            const T* src = static_cast<const T*>(mat(which).data) + row * mat(which).ld + c;
+            copy_async16(slot(stage, which, v), src);
+            if constexpr (sizeof(T) == 4) copy_async16(slot(stage, which, v) + 16, src + 4);
+          }
+        }
       }
     }
-    cta_sum<3>(sum, slot);
+  }
+  // The exponent bytes of a row, asked for one row ahead.
+  __device__ __forceinline__ void fetch_scales(int64_t row) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (packed(kInY + k) && present(kInY + k))
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int c = column<true>(v, 0, t, p.tpr);
+            next[k][v] = 0;
+            if (c < p.cols)
+              next[k][v] = act(kInY + k).exps[row * act(kInY + k).ld_exps + c / kAct8Block];
+          }
+    }
+  }
+  __device__ __forceinline__ void take_scales() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (packed(kInY + k) && present(kInY + k))
+#pragma unroll
+          for (int v = 0; v < NV; ++v) scale[k][v] = act8_scale(next[k][v]);
+    }
+  }
+
+  __device__ __forceinline__ void get(int64_t row, int stage, int which, int v,
+                                      float (&f)[8]) const {
+    if constexpr (VEC) {
+      if (!present(which) || column<true>(v, 0, t, p.tpr) >= p.cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        return;
+      }
+      const uint32_t a = slot(stage, which, v);
+      if (packed(which)) {
+        uint2 c;
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(a) : "memory");
+        act8_values(c, scale[which - kInY][v], f);
+        return;
+      }
+      Raw8<T> r;
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
+                   : "r"(a)
+                   : "memory");
+      if constexpr (sizeof(T) == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.w.x), "=r"(r.w.y), "=r"(r.w.z), "=r"(r.w.w)
+                     : "r"(a + 16)
+                     : "memory");
+      widen8<T>(r, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      if (!present(which)) return;
+      if (packed(which)) {
+        const Act8Out& o = act(which);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = column<false>(v, i, t, p.tpr);
+          if (c < p.cols)
+            f[i] = (float)o.codes[row * o.ld_codes + c] *
+                   act8_scale(o.exps[row * o.ld_exps + c / kAct8Block]);
+        }
+      } else {
+        const T* q = static_cast<const T*>(mat(which).data) + row * mat(which).ld;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = column<false>(v, i, t, p.tpr);
+          if (c < p.cols) f[i] = to_f32(q[c]);
+        }
+      }
+    }
+  }
+};
+
+// At the end of a gate row's rows in a part: its sums branch_scale * e (in `mine`)
+// go into dw_post's and into dgate, or into a partial row of it.
+template <bool VEC, int NV>
+__device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t part, int64_t lo,
+                                            int64_t hi, int64_t row, bool first_gate, int t,
+                                            float* post, const float* mine, int stride) {
+  int64_t glo, ghi;
+  gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
+  const bool inside = glo >= lo && ghi <= hi;
+  const int64_t grow = gate_row_of(p.gate_rows, row);
+  float* out = part_row(p, part, first_gate ? kPartGateFirst : kPartGateLast);
+#pragma unroll 1
+  for (int v = 0; v < NV; ++v)
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<VEC>(v, i, t, p.tpr);
+      if (c >= p.cols) continue;
+      const float x = mine[(v * 8 + i) * stride];
+      const float g = p.gate.data ? ld_any(p.gate.data, p.param_dtype, grow * p.gate.ld + c) : 1.f;
+      const float w = p.w_post ? ld_any(p.w_post, p.param_dtype, c) : 1.f;
+      post[(v * 8 + i) * stride] = fmaf(g, x, post[(v * 8 + i) * stride]);
+      if (!p.dgate.data) continue;
+      if (inside)
+        st_any(p.dgate.data, p.param_dtype, grow * p.dgate.ld + c, w * x);
+      else
+        out[c] = w * x;
+    }
+}
+
+// One group of threads per run of rows.  Per row one reading forms three sums,
+//   s = <w_pre du, h>,  a = <q, dh_out + r1 w_pre du>,  b = <q, h>,  q = w_post gate y,
+// from which <w_post dz, y> = branch (a - r1^3 s / C b); a second reading forms
+// the outputs.  Sums over rows per column: dw_pre, and e = sum d y rstd_post,
+// from which, while the gate row stays the same, dw_post grows by branch gate e
+// and dgate is branch w_post e.
+template <class T, bool VEC, int NV>
+__global__ void __launch_bounds__(kJoinCta, 1)
+    block_join_grad_kernel(const __grid_constant__ JoinGradParams p) {
+  pdl_enter();
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ float slot[2][kJoinCta / 32][3];
+  const int group = threadIdx.x / p.tpr, t = threadIdx.x - group * p.tpr;
+  const int64_t parts = part_count(p.rows, p.cols), per = part_rows(p.rows, p.cols);
+  const int64_t part = (int64_t)blockIdx.x * p.groups + group;
+  if (part >= parts || !dbg_ok(p.dbg, p.tpr * 8 * NV >= p.cols)) return;
+  const int64_t lo = part * per, hi = min(p.rows, lo + per);
+  const float inv_c = 1.f / (float)p.cols;
+  // dw_post of finished gate rows, one place per column of a thread
+  const int stride = blockDim.x;
+  float* post = reinterpret_cast<float*>(dyn) + threadIdx.x;
+  float* mine = post + 8 * NV * stride;  // parameters and sums on their way
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dyn) +
+                        16 * NV * stride * (uint32_t)sizeof(float) +
+                        group * p.stages * p.stage_bytes;
+  GradRow<T, VEC, NV> in(p, t, ring);
+  float wpre[NV][8], q[NV][8], acc[NV][8], e[NV][8];
+  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      wpre[v][i] = mine[(v * 8 + i) * stride];
+      acc[v][i] = e[v][i] = 0.f;
+      post[(v * 8 + i) * stride] = 0.f;
+    }
+  for (int s = 0; s < p.stages; ++s) {
+    if (lo + s < hi) in.fetch(lo + s, s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  in.fetch_scales(lo);
+  int64_t held = -1;
+  bool first_gate = true;
+  int stage = 0;
+  for (int64_t row = lo; row < hi; ++row) {
+    const int64_t grow = gate_row_of(p.gate_rows, row);
+    if (grow != held) {
+      held = grow;
+      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[v][i] = mine[(v * 8 + i) * stride];
+      if (p.gate.data) {
+        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, p.tpr, p.cols, mine,
+                             stride);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[v][i] *= mine[(v * 8 + i) * stride];
+      }
+    }
+    const float r1 = p.du.data ? p.rstd_pre[row] : 0.f;
+    const float r2 = p.rstd_post ? p.rstd_post[row] : 1.f;
+    in.take_scales();
+    if (row + 1 < hi) in.fetch_scales(row + 1);
+    if constexpr (VEC) {
+      // the oldest of the rows asked for has arrived
+      if (p.stages == 1)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else if (p.stages == 2)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    }
+    float sum[3] = {0.f, 0.f, 0.f};
+    {
+      uint64_t s2 = 0, a2 = 0, b2 = 0;
+      const uint64_t rr = pair(r1, r1);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float d[8], u[8], h[8], y[8];
+        in.get(row, stage, kInDh, v, d);
+        in.get(row, stage, kInDu, v, u);
+        in.get(row, stage, kInY, v, y);
+        in.get(row, stage, kInH, v, h);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint64_t wu = mul2(pair(wpre[v][i], wpre[v][i + 1]), pair(u[i], u[i + 1]));
+          const uint64_t qy = mul2(pair(q[v][i], q[v][i + 1]), pair(y[i], y[i + 1]));
+          const uint64_t hh = pair(h[i], h[i + 1]);
+          s2 = fma2(wu, hh, s2);
+          a2 = fma2(qy, fma2(rr, wu, pair(d[i], d[i + 1])), a2);
+          b2 = fma2(qy, hh, b2);
+        }
+      }
+      sum[0] = lane0(s2) + lane1(s2);
+      sum[1] = lane0(a2) + lane1(a2);
+      sum[2] = lane0(b2) + lane1(b2);
+    }
+    group_sum<3>(sum, slot[row & 1], group, p.tpr);
     const float k1 = r1 * r1 * r1 * sum[0] * inv_c;
     const float k2 = p.rstd_post
                          ? r2 * r2 * r2 * p.branch_scale * (sum[1] - k1 * sum[2]) * inv_c
                          : 0.f;
-    for (int64_t gi = threadIdx.x; gi < p.groups; gi += kJoinThreads) {
-      const int64_t col = gi * 8;
-      float d[8], t[8], h[8], y[8], wp[8], g[8], w[8];
-      load(col, d, t, h, y, wp, g);
-      weight8(p.w_pre, p.param_dtype, col, p.cols, w);
-      float dh[8], dy[8];
+    const float c1 = r2 * p.branch_scale;
+    {
+      const uint64_t r1p = pair(r1, r1), r2p = pair(r2, r2), k1p = pair(-k1, -k1),
+                     k2p = pair(-k2, -k2), c1p = pair(c1, c1),
+                     resp = pair(p.res_scale, p.res_scale);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float full = fmaf(r1, w[i] * t[i], d[i]) - k1 * h[i];
-        const float dz = p.branch_scale * g[i] * full;
-        dh[i] = p.res_scale * full;
-        dy[i] = p.rstd_post ? r2 * wp[i] * dz - k2 * y[i] : dz;
-        acc[col + i] = fmaf(t[i], h[i] * r1, acc[col + i]);
-        acc[width + col + i] = fmaf(dz, y[i] * r2, acc[width + col + i]);
-        acc[2 * width + col + i] =
-            fmaf(p.branch_scale * full, y[i] * r2 * wp[i], acc[2 * width + col + i]);
+      for (int v = 0; v < NV; ++v) {
+        float d[8], u[8], h[8], y[8];
+        in.get(row, stage, kInDh, v, d);
+        in.get(row, stage, kInDu, v, u);
+        in.get(row, stage, kInY, v, y);
+        in.get(row, stage, kInH, v, h);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint64_t u2 = pair(u[i], u[i + 1]), y2 = pair(y[i], y[i + 1]);
+          const uint64_t h2 = pair(h[i], h[i + 1]);
+          const uint64_t lin = fma2(r1p, mul2(pair(wpre[v][i], wpre[v][i + 1]), u2),
+                                    pair(d[i], d[i + 1]));
+          const uint64_t full = fma2(k1p, h2, lin);
+          const uint64_t ac = fma2(u2, mul2(h2, r1p), pair(acc[v][i], acc[v][i + 1]));
+          const uint64_t ee = fma2(full, mul2(y2, r2p), pair(e[v][i], e[v][i + 1]));
+          const uint64_t dh = mul2(full, resp);
+          const uint64_t dy =
+              fma2(k2p, y2, mul2(pair(q[v][i], q[v][i + 1]), mul2(full, c1p)));
+          acc[v][i] = lane0(ac);
+          acc[v][i + 1] = lane1(ac);
+          e[v][i] = lane0(ee);
+          e[v][i + 1] = lane1(ee);
+          d[i] = lane0(dh);
+          d[i + 1] = lane1(dh);
+          u[i] = lane0(dy);
+          u[i + 1] = lane1(dy);
+        }
+        if (p.dh.data) frag_store<T, VEC>(p.dh, row, v, t, p.tpr, p.cols, d);
+        frag_store<T, VEC>(p.dy, row, v, t, p.tpr, p.cols, u);
       }
-      if (p.dh.data) mat_store8<T>(p.dh, row, col, p.cols, dh);
-      mat_store8<T>(p.dy, row, col, p.cols, dy);
     }
-    if (p.dgate.data) {
-      int64_t glo, ghi;
-      gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
-      if (row + 1 == hi || row + 1 == ghi) {  // the last row here of its gate row
-        const bool inside = glo >= lo && ghi <= hi;
-        float* out = part_row(p, part, first_gate ? kPartGateFirst : kPartGateLast);
-        for (int64_t gi = threadIdx.x; gi < p.groups; gi += kJoinThreads)
-          for (int64_t col = gi * 8; col < gi * 8 + 8; ++col) {
-            if (col >= p.cols) continue;
-            const float x = acc[2 * width + col];
-            if (inside)
-              st_any(p.dgate.data, p.param_dtype, grow * p.dgate.ld + col, x);
-            else
-              out[col] = x;
-            acc[2 * width + col] = 0.f;
-          }
-        first_gate = false;
-      }
+    if constexpr (VEC) {
+      if (row + p.stages < hi) in.fetch(row + p.stages, stage);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      stage = stage + 1 == p.stages ? 0 : stage + 1;
+    }
+    if (row + 1 == hi || gate_row_of(p.gate_rows, row + 1) != grow) {
+      // the last row here of its gate row
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mine[(v * 8 + i) * stride] = p.branch_scale * e[v][i];
+          e[v][i] = 0.f;
+        }
+      close_gate_row<VEC, NV>(p, part, lo, hi, row, first_gate, t, post, mine, stride);
+      first_gate = false;
     }
   }
-  for (int64_t gi = threadIdx.x; gi < p.groups; gi += kJoinThreads)
-    for (int64_t col = gi * 8; col < gi * 8 + 8; ++col) {
-      if (p.dw_pre) part_row(p, part, kPartWPre)[col] = acc[col];
-      if (p.dw_post) part_row(p, part, kPartWPost)[col] = acc[width + col];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<VEC>(v, i, t, p.tpr);
+      if (c >= p.cols) continue;
+      if (p.dw_pre) part_row(p, part, kPartWPre)[c] = acc[v][i];
+      if (p.dw_post) part_row(p, part, kPartWPost)[c] = post[(v * 8 + i) * stride];
     }
 }
 
@@ -299,10 +681,10 @@ __global__ void __launch_bounds__(kJoinThreads) block_join_grad_kernel(const Joi
 constexpr int kFinishRuns = 8;
 
 __global__ void __launch_bounds__(32 * kFinishRuns)
-block_join_finish_kernel(const JoinGradParams p) {
+block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   __shared__ float run_sum[kFinishRuns][33];
-  const int64_t parts = part_count(p.rows), per = part_rows(p.rows);
+  const int64_t parts = part_count(p.rows, p.cols), per = part_rows(p.rows, p.cols);
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   int slot = blockIdx.y;
@@ -374,9 +756,20 @@ bool same(const dpopt_matrix& a, const dpopt_matrix& b, int64_t rows) {
   return a.data == b.data && (rows <= 1 || a.ld == b.ld);
 }
 
-int64_t round_groups(int64_t cols) {
-  return (cols + kAct8Block - 1) / kAct8Block * (kAct8Block / 8);
+int64_t whole_blocks(int64_t cols) {
+  return (cols + kAct8Block - 1) / kAct8Block * kAct8Block;
 }
+
+// Rows (or runs of rows) at a time in a CTA: at most `most`, and fewer when there
+// are too few to give every SM a CTA.
+int group_count(int most, int64_t rows) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (rows + kJoinSms - 1) / kJoinSms));
+}
+
+bool vec_ok(const Mat& m) { return !m.data || m.vec; }
+bool vec_ok(const Act8Out& a) { return !a.codes || a.vec; }
+
+constexpr size_t kJoinSmem = 220 * 1024;  // of 227 KB; the static arrays need some
 
 template <class K>
 int allow_smem(K kern, size_t bytes) {
@@ -384,6 +777,75 @@ int allow_smem(K kern, size_t bytes) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   return e == cudaSuccess ? DPOPT_OK : cuda_fail(e, "shared memory size");
+}
+
+template <class T, bool VEC, int NV>
+int launch_join_at(JoinParams& p, cudaStream_t stream) {
+  auto kern = block_join_kernel<T, VEC, NV>;
+  int sms = 0, per_sm = 0;
+  DPOPT_TRY(sm_count(&sms));
+  p.groups = group_count(std::max(1, std::min(15, 256 / p.tpr)), p.rows);
+  const int threads = p.groups * p.tpr;
+  const size_t smem = (size_t)threads * 8 * NV * sizeof(float);
+  DPOPT_TRY(allow_smem(kern, smem));
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "block join occupancy");
+  const int64_t ctas = (p.rows + p.groups - 1) / p.groups;
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * std::max(per_sm, 1));
+  return launched(launch_pdl(kern, grid, threads, smem, stream, p), "block join");
+}
+
+template <class T>
+int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
+  switch (row_frags(p.cols)) {
+    case 1:
+      return vec ? launch_join_at<T, true, 1>(p, stream) : launch_join_at<T, false, 1>(p, stream);
+    case 2:
+      return vec ? launch_join_at<T, true, 2>(p, stream) : launch_join_at<T, false, 2>(p, stream);
+    default:
+      return vec ? launch_join_at<T, true, 4>(p, stream) : launch_join_at<T, false, 4>(p, stream);
+  }
+}
+
+template <class T, bool VEC, int NV>
+int launch_join_grad_at(JoinGradParams& p, cudaStream_t stream) {
+  auto kern = block_join_grad_kernel<T, VEC, NV>;
+  const int64_t parts = part_count(p.rows, p.cols);
+  p.groups = group_count(groups_most(p.cols), parts);
+  const int threads = p.groups * p.tpr;
+  const size_t post = (size_t)threads * 16 * NV * sizeof(float);
+  const size_t row = (size_t)p.stage_bytes * p.groups;
+  p.stages = VEC ? (int)std::min<size_t>(3, (kJoinSmem - post) / row) : 0;
+  const size_t smem = post + p.stages * row;
+  DPOPT_TRY(allow_smem(kern, smem));
+  const unsigned grid = (unsigned)((parts + p.groups - 1) / p.groups);
+  return launched(launch_pdl(kern, grid, threads, smem, stream, p), "block join gradient");
+}
+
+template <class T>
+int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
+  const int nv = row_frags(p.cols), groups = groups_most(p.cols);
+  p.stage_bytes = 0;
+  for (int which = 0; which < 4; ++which) {
+    const bool packed = (which == kInY && p.y8.codes) || (which == kInH && p.h8.codes);
+    p.frag_at[which] = p.stage_bytes;
+    p.frag_bytes[which] = packed ? 8 : 8 * sizeof(T);
+    if (which == kInDh || which == kInY || p.du.data)
+      p.stage_bytes += p.frag_bytes[which] * nv * p.tpr;
+  }
+  // the vector form needs room for at least one row of the ring
+  vec = vec && (size_t)groups * (p.tpr * 16 * nv * sizeof(float) + p.stage_bytes) <= kJoinSmem;
+  switch (nv) {
+    case 1:
+      return vec ? launch_join_grad_at<T, true, 1>(p, stream)
+                 : launch_join_grad_at<T, false, 1>(p, stream);
+    case 2:
+      return vec ? launch_join_grad_at<T, true, 2>(p, stream)
+                 : launch_join_grad_at<T, false, 2>(p, stream);
+    default:
+      return vec ? launch_join_grad_at<T, true, 4>(p, stream)
+                 : launch_join_grad_at<T, false, 4>(p, stream);
+  }
 }
 
 }  // namespace
@@ -419,22 +881,22 @@ int dpopt_block_join(const dpopt_block_join_args* a, dpopt_stream_t stream) {
   if (a->gate.data)
     DPOPT_TRY(take_matrix("gate", a->gate, gate_count(rows, a->gate_rows), cols, ps, false,
                           &p.gate, s, &n));
-  auto vec = [&](const char* name, const void* q, int64_t len, int64_t size, bool w) {
+  auto one = [&](const char* name, const void* q, int64_t len, int64_t size, bool w) {
     return q ? take_matrix(name, dpopt_matrix{const_cast<void*>(q), len}, 1, len, size, w, &dummy,
                            s, &n)
              : DPOPT_OK;
   };
-  DPOPT_TRY(vec("w_post", a->w_post, cols, ps, false));
-  DPOPT_TRY(vec("w_pre", a->w_pre, cols, ps, false));
-  DPOPT_TRY(vec("rstd_post", a->rstd_post, rows, 4, true));
-  DPOPT_TRY(vec("rstd_pre", a->rstd_pre, rows, 4, true));
+  DPOPT_TRY(one("w_post", a->w_post, cols, ps, false));
+  DPOPT_TRY(one("w_pre", a->w_pre, cols, ps, false));
+  DPOPT_TRY(one("rstd_post", a->rstd_post, rows, 4, true));
+  DPOPT_TRY(one("rstd_pre", a->rstd_pre, rows, 4, true));
   if (a->y8.codes) DPOPT_TRY(take_act8("y8", a->y8, rows, cols, true, &p.y8, s, &n));
   if (a->h8.codes) DPOPT_TRY(take_act8("h8", a->h8, rows, cols, true, &p.h8, s, &n));
   if (a->u8.codes) DPOPT_TRY(take_act8("u8", a->u8, rows, cols, true, &p.u8, s, &n));
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
   p.cols = cols;
-  p.groups = round_groups(cols);
+  p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.eps = a->eps;
   p.res_scale = a->res_scale;
@@ -445,16 +907,12 @@ int dpopt_block_join(const dpopt_block_join_args* a, dpopt_stream_t stream) {
   p.rstd_post = a->rstd_post;
   p.rstd_pre = a->rstd_pre;
   p.dbg = make_dbg();
-  int sms = 0;
-  DPOPT_TRY(sm_count(&sms));
-  auto kern = a->dtype == DPOPT_GRAD_BF16  ? block_join_kernel<bf16>
-              : a->dtype == DPOPT_GRAD_F16 ? block_join_kernel<fp16>
-                                           : block_join_kernel<float>;
-  const size_t smem = (size_t)p.groups * 8 * sizeof(float);
-  DPOPT_TRY(allow_smem(kern, smem));
-  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)sms * 8);
-  return launched(launch_pdl(kern, grid, kJoinThreads, smem, (cudaStream_t)stream, p),
-                  "block join");
+  const bool vec = cols % 8 == 0 && vec_ok(p.h) && vec_ok(p.y) && vec_ok(p.h_out) &&
+                   vec_ok(p.u) && vec_ok(p.y8) && vec_ok(p.h8) && vec_ok(p.u8);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (a->dtype == DPOPT_GRAD_BF16) return launch_join<bf16>(p, vec, st);
+  if (a->dtype == DPOPT_GRAD_F16) return launch_join<fp16>(p, vec, st);
+  return launch_join<float>(p, vec, st);
 }
 
 int dpopt_block_join_scratch_bytes(int64_t rows, int64_t cols, int64_t gate_rows,
@@ -464,7 +922,8 @@ int dpopt_block_join_scratch_bytes(int64_t rows, int64_t cols, int64_t gate_rows
   if (cols > DPOPT_JOIN_MAX_COLS)
     return fail(DPOPT_ERR_UNSUPPORTED, "cols %lld exceeds %d", (long long)cols,
                 DPOPT_JOIN_MAX_COLS);
-  *bytes_out = part_count(rows) * kPartSlots * round_groups(cols) * 8 * (int64_t)sizeof(float);
+  *bytes_out = part_count(rows, cols) * kPartSlots * whole_blocks(cols) *
+               (int64_t)sizeof(float);
   return DPOPT_OK;
 }
 
@@ -511,17 +970,17 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   if (a->dgate.data)
     DPOPT_TRY(take_matrix("dgate", a->dgate, gates, cols, ps, true, &p.dgate, s, &n));
   Mat dummy;
-  auto vec = [&](const char* name, const void* q, int64_t len, int64_t size, bool w) {
+  auto one = [&](const char* name, const void* q, int64_t len, int64_t size, bool w) {
     return q ? take_matrix(name, dpopt_matrix{const_cast<void*>(q), len}, 1, len, size, w, &dummy,
                            s, &n)
              : DPOPT_OK;
   };
-  DPOPT_TRY(vec("w_post", a->w_post, cols, ps, false));
-  DPOPT_TRY(vec("w_pre", a->w_pre, cols, ps, false));
-  DPOPT_TRY(vec("rstd_post", a->rstd_post, rows, 4, false));
-  DPOPT_TRY(vec("rstd_pre", a->rstd_pre, rows, 4, false));
-  DPOPT_TRY(vec("dw_post", a->dw_post, cols, ps, true));
-  DPOPT_TRY(vec("dw_pre", a->dw_pre, cols, ps, true));
+  DPOPT_TRY(one("w_post", a->w_post, cols, ps, false));
+  DPOPT_TRY(one("w_pre", a->w_pre, cols, ps, false));
+  DPOPT_TRY(one("rstd_post", a->rstd_post, rows, 4, false));
+  DPOPT_TRY(one("rstd_pre", a->rstd_pre, rows, 4, false));
+  DPOPT_TRY(one("dw_post", a->dw_post, cols, ps, true));
+  DPOPT_TRY(one("dw_pre", a->dw_pre, cols, ps, true));
   int64_t need = 0;
   DPOPT_TRY(dpopt_block_join_scratch_bytes(rows, cols, a->gate_rows, &need));
   if (need > 0) {
@@ -530,12 +989,12 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
     if (a->scratch_bytes < need)
       return fail(DPOPT_ERR_INVALID_ARG, "scratch holds %lld bytes, %lld are needed",
                   (long long)a->scratch_bytes, (long long)need);
-    DPOPT_TRY(vec("scratch", a->scratch, need, 1, true));
+    DPOPT_TRY(one("scratch", a->scratch, need, 1, true));
   }
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
   p.cols = cols;
-  p.groups = round_groups(cols);
+  p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.res_scale = a->res_scale;
   p.branch_scale = a->branch_scale;
@@ -548,16 +1007,16 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   p.dw_pre = a->dw_pre;
   p.partial = static_cast<float*>(a->scratch);
   p.dbg = make_dbg();
-  const int64_t parts = part_count(rows);
+  const int64_t parts = part_count(rows, cols);
+  p.width = whole_blocks(cols);
   if (rows > 0) {
-    auto kern = a->dtype == DPOPT_GRAD_BF16  ? block_join_grad_kernel<bf16>
-                : a->dtype == DPOPT_GRAD_F16 ? block_join_grad_kernel<fp16>
-                                             : block_join_grad_kernel<float>;
-    const size_t smem = (size_t)p.groups * 8 * 3 * sizeof(float);
-    DPOPT_TRY(allow_smem(kern, smem));
-    DPOPT_TRY(launched(
-        launch_pdl(kern, (unsigned)parts, kJoinThreads, smem, (cudaStream_t)stream, p),
-        "block join gradient"));
+    const bool vec = cols % 8 == 0 && vec_ok(p.dh_out) && vec_ok(p.du) && vec_ok(p.y) &&
+                     vec_ok(p.h_out) && vec_ok(p.dh) && vec_ok(p.dy) && vec_ok(p.y8) &&
+                     vec_ok(p.h8);
+    const cudaStream_t st = (cudaStream_t)stream;
+    DPOPT_TRY(a->dtype == DPOPT_GRAD_BF16  ? launch_join_grad<bf16>(p, vec, st)
+              : a->dtype == DPOPT_GRAD_F16 ? launch_join_grad<fp16>(p, vec, st)
+                                           : launch_join_grad<float>(p, vec, st));
   }
   if (!p.dw_pre && !p.dw_post && !p.dgate.data) return DPOPT_OK;
   // gate rows that cross a part's border: one for all rows, or at most one per
@@ -566,7 +1025,7 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   if (p.dgate.data) {
     if (a->gate_rows == 0)
       gate_sums = rows == 0 || parts > 1;
-    else if (rows > 0 && part_rows(rows) % a->gate_rows != 0)
+    else if (rows > 0 && part_rows(rows, cols) % a->gate_rows != 0)
       gate_sums = (unsigned)(parts - 1);
   }
   if (!p.dw_pre && !p.dw_post && gate_sums == 0) return DPOPT_OK;

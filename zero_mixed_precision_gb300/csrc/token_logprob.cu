@@ -49,9 +49,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// 2^x to two units in the last place; results below 2^-126 are 0 (keeping them
+// would cost three more instructions for each logit).
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -107,30 +109,6 @@ __device__ __forceinline__ void extremes(const Raw8<float>& r, float& hi, float&
     hi = max_nan(hi, f[i]);
     lo = fminf(lo, f[i]);
   }
-}
-
-// Two fp32 lanes in one instruction (sm_100 and later).
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ float lane0(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float lane1(uint64_t x) {
-  return __uint_as_float((uint32_t)(x >> 32));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // Logits of at least this magnitude are left out of the running softmax (below
@@ -201,50 +179,43 @@ struct Running {
   }
 };
 
-// (max, ref, sum, ent) of two disjoint sets, brought to the larger ref.
-__device__ __forceinline__ TokPartial merge(const TokPartial& a, const TokPartial& b) {
-  TokPartial r;
-  r.max = max_nan(a.max, b.max);
-  r.ref = fmaxf(a.ref, b.ref);
-  r.sum = r.ent = 0.f;
-  // a set without terms has ref = -Inf; a NaN sum is kept
-  if (a.sum != 0.f) {
-    const float d = a.ref - r.ref, f = exp2_approx(d);
-    r.sum += f * a.sum;
-    r.ent += f * fmaf(d, a.sum, a.ent);
+// The sets of the lanes that differ in the bits of `lanes` (1, 2, .. up to it)
+// joined, the same bits in each: all are brought to the largest ref, then added.
+__device__ __forceinline__ TokPartial lanes_merge(TokPartial p, int lanes) {
+  float ref = p.ref;
+  for (int o = lanes; o > 0; o >>= 1) {
+    p.max = max_nan(p.max, __shfl_xor_sync(0xffffffffu, p.max, o));
+    ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
   }
-  if (b.sum != 0.f) {
-    const float d = b.ref - r.ref, f = exp2_approx(d);
-    r.sum += f * b.sum;
-    r.ent += f * fmaf(d, b.sum, b.ent);
+  if (p.sum != 0.f) {  // a set without terms has ref = -Inf; a NaN sum is kept
+    const float d = p.ref - ref, f = exp2_approx(d);
+    p.ent = f * fmaf(d, p.sum, p.ent);
+    p.sum *= f;
   }
-  return r;
+  for (int o = lanes; o > 0; o >>= 1) {
+    p.sum += __shfl_xor_sync(0xffffffffu, p.sum, o);
+    p.ent += __shfl_xor_sync(0xffffffffu, p.ent, o);
+  }
+  p.ref = ref;
+  return p;
 }
 
 struct TokShared {
   TokPartial part[kTokWarps];
   float slot[kTokWarps];
   uint64_t kslot[kTokWarps];
-  uint32_t group[32];
-  int found;
+  uint32_t group[32], floor;
+  int found, agains;
+  uint8_t again[kTokThreads];
   uint64_t cand[1024];
   uint64_t best[DPOPT_MAX_TOP];
 };
 
 __device__ __forceinline__ TokPartial cta_merge(TokPartial p, TokShared& sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const TokPartial q{__shfl_down_sync(0xffffffffu, p.max, o),
-                       __shfl_down_sync(0xffffffffu, p.ref, o),
-                       __shfl_down_sync(0xffffffffu, p.sum, o),
-                       __shfl_down_sync(0xffffffffu, p.ent, o)};
-    p = merge(p, q);
-  }
+  p = lanes_merge(p, 16);
   if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = p;
   __syncthreads();
-  p = sh.part[0];
-  for (int w = 1; w < kTokWarps; ++w) p = merge(p, sh.part[w]);
-  return p;
+  return lanes_merge(sh.part[threadIdx.x % kTokWarps], kTokWarps / 2);
 }
 
 // The stretch [lo, hi) of a row as head elements up to a 16-byte boundary,
@@ -297,26 +268,35 @@ __device__ void stretch_top(const Stretch<T>& st, int64_t lo, int top, float thr
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
   if ((threadIdx.x & 7) == 0) sh.group[threadIdx.x >> 3] = g;
-  if (threadIdx.x == 0) sh.found = 0;
+  if (threadIdx.x == 0) sh.found = sh.agains = 0;
   __syncthreads();
-  g = sh.group[threadIdx.x & 31];
-  int rank = 0;
+  if (threadIdx.x < 32) {
+    g = sh.group[threadIdx.x];
+    int rank = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t o = __shfl_sync(0xffffffffu, g, j);
-    rank += o > g || (o == g && j < (int)(threadIdx.x & 31));
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t o = __shfl_sync(0xffffffffu, g, j);
+      rank += o > g || (o == g && j < (int)threadIdx.x);
+    }
+    if (rank == top - 1) sh.floor = g;
   }
-  const uint32_t at = __ballot_sync(0xffffffffu, rank == top - 1);
-  const uint32_t floor = __shfl_sync(0xffffffffu, g, __ffs(at) - 1);
+  __syncthreads();
+  const uint32_t floor = sh.floor;
+  const float floor_value = rank_value(floor);  // a NaN lets everything pass
   auto offer = [&](float x, int64_t i) {
-    if (rank_bits(x) < floor) return;
+    if (x < floor_value) return;
     const int n = atomicAdd(&sh.found, 1);  // the order in the list does not matter
     if (n < (int)(sizeof(sh.cand) / 8)) sh.cand[n] = rank_key(x, (uint32_t)(lo + i));
   };
-  if (mine >= floor) {
-    for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads)
-      offer(to_f32(st.x[st.loose_at(t)]), st.loose_at(t));
-    for (int64_t v = threadIdx.x; v < st.vecs; v += kTokThreads) {
+  // the threads to look at again, then a warp for each: lane i takes the thread's
+  // i-th vector, so that they are all in flight at once
+  if (mine >= floor) sh.again[atomicAdd(&sh.agains, 1)] = (uint8_t)threadIdx.x;
+  __syncthreads();
+  const int agains = sh.agains, lane = threadIdx.x & 31;
+  for (int a = threadIdx.x >> 5; a < agains; a += kTokWarps) {
+    const int64_t t = sh.again[a];
+    if (lane == 0 && t < st.loose()) offer(to_f32(st.x[st.loose_at(t)]), st.loose_at(t));
+    for (int64_t v = t + lane * kTokThreads; v < st.vecs; v += 32 * kTokThreads) {
       float f[8];
       widen8<T>(ld_raw8<T>(st.x + st.head + v * 8), f);
 #pragma unroll
