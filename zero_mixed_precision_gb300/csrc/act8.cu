@@ -1,50 +1,118 @@
 // act8.cu -- activations packed into 8 bits and restored (the format is stated
-// in include/dpopt.h): one block of 32 columns is four threads of eight.
+// in include/dpopt.h).
 #include "ops.cuh"
 
 namespace dpopt {
 namespace {
 
+// The work is cut into units of 256 columns of a row, one for a warp; a warp's
+// next unit is `step` further on, taken as whole rows and units so that no unit
+// needs a division.
 struct Act8Params {
-  int64_t rows, cols;
-  int64_t groups;  // 8-column groups of one row, rounded up to whole blocks of four
+  int64_t rows;
+  int cols, units;  // units of a row
+  int64_t step_rows;
+  int step_units;
   Mat x;
   Act8Out packed;
   Dbg dbg;
 };
 
-constexpr int kActThreads = 256;
+constexpr int kActThreads = 256, kActUnit = 256;
 
-template <class T>
-__global__ void __launch_bounds__(kActThreads) act8_pack_kernel(const Act8Params p) {
+struct UnitWalk {
+  int64_t row;
+  int unit;
+  __device__ __forceinline__ explicit UnitWalk(const Act8Params& p) {
+    const int64_t first = ((int64_t)blockIdx.x * kActThreads + threadIdx.x) >> 5;
+    row = first / p.units;
+    unit = (int)(first - row * p.units);
+  }
+  __device__ __forceinline__ void next(const Act8Params& p) {
+    row += p.step_rows;
+    unit += p.step_units;
+    if (unit >= p.units) {
+      unit -= p.units;
+      ++row;
+    }
+  }
+};
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    act8_pack_kernel(const __grid_constant__ Act8Params p) {
   pdl_enter();
-  const int64_t total = p.rows * p.groups;  // a multiple of 4: blocks stay in one warp
-  const int64_t stride = (int64_t)gridDim.x * kActThreads;
-  const int64_t rounds = (total + stride - 1) / stride;
-  int64_t g = (int64_t)blockIdx.x * kActThreads + threadIdx.x;
-  for (int64_t it = 0; it < rounds; ++it, g += stride) {
-    // threads past the end keep step with their warp on columns past the row's
-    const bool live = g < total && dbg_ok(p.dbg, g / p.groups < p.rows);
-    const int64_t row = live ? g / p.groups : 0;
-    const int64_t col = live ? (g - row * p.groups) * 8 : p.groups * 8;
+  const int lane = threadIdx.x & 31;
+  UnitWalk at(p);
+  Frag<T, VEC> ahead;
+  if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kActUnit);
+  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.units)) {
+    const int64_t row = at.row;
+    const int c0 = at.unit * kActUnit;
     float f[8];
-    mat_load8<T>(p.x, row, col, p.cols, f);
-    act8_store8<T>(p.packed, row, col, p.cols, f);
+    ahead.widen(f);
+    at.next(p);
+    if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kActUnit);
+    frag_pack<T, VEC>(p.packed, row, 0, lane, 32, p.cols, f, c0);
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kActThreads) act8_unpack_kernel(const Act8Params p) {
+// The vector form: a thread's 8 columns at once; the element form: each lane its
+// column of the unit's 8 blocks.
+template <bool VEC>
+struct CodeFrag;
+template <>
+struct CodeFrag<true> {
+  uint2 c;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
+    const int col = c0 + lane * 8;
+    c = make_uint2(0, 0);
+    byte = 0;
+    if (col >= cols) return;
+    c = *reinterpret_cast<const uint2*>(o.codes + row * o.ld_codes + col);
+    byte = o.exps[row * o.ld_exps + col / kAct8Block];
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    act8_values(c, act8_scale(byte), f);
+  }
+};
+template <>
+struct CodeFrag<false> {
+  int8_t c[8];
+  uint8_t byte[8];
+  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
+    const int8_t* codes = o.codes + row * o.ld_codes;
+    const uint8_t* exps = o.exps + row * o.ld_exps;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = c0 + i * 32 + lane;
+      c[i] = col < cols ? codes[col] : 0;
+      byte[i] = col < cols ? exps[col / kAct8Block] : 0;
+    }
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)c[i] * act8_scale(byte[i]);
+  }
+};
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    act8_unpack_kernel(const __grid_constant__ Act8Params p) {
   pdl_enter();
-  const int64_t total = p.rows * p.groups;
-  const int64_t stride = (int64_t)gridDim.x * kActThreads;
-  for (int64_t g = (int64_t)blockIdx.x * kActThreads + threadIdx.x; g < total; g += stride) {
-    const int64_t row = g / p.groups;
-    const int64_t col = (g - row * p.groups) * 8;
-    if (!dbg_ok(p.dbg, row < p.rows)) continue;
+  const int lane = threadIdx.x & 31;
+  UnitWalk at(p);
+  CodeFrag<VEC> ahead;
+  if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kActUnit);
+  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.units)) {
+    const int64_t row = at.row;
+    const int c0 = at.unit * kActUnit;
     float f[8];
-    act8_load8(p.packed, row, col, p.cols, f);
-    mat_store8<T>(p.x, row, col, p.cols, f);
+    ahead.values(f);
+    at.next(p);
+    if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kActUnit);
+    frag_store<T, VEC>(p.x, row, 0, lane, 32, p.cols, f, c0);
   }
 }
 
@@ -59,21 +127,28 @@ int prepare(Act8Params& p, bool pack, void* x, int dtype, int64_t rows, int64_t 
   DPOPT_TRY(take_act8("the packed matrix", dpopt_act8{codes, ld_codes, exps, ld_exps}, rows, cols,
                       pack, &p.packed, s, &n));
   DPOPT_TRY(check_overlaps(s, n));
+  if (cols > INT32_MAX - kActUnit) return fail(DPOPT_ERR_UNSUPPORTED, "cols must be below 2^31");
   p.rows = rows;
-  p.cols = cols;
-  p.groups = (cols + kAct8Block - 1) / kAct8Block * (kAct8Block / 8);
+  p.cols = (int)cols;
+  p.units = (int)((cols + kActUnit - 1) / kActUnit);
   p.dbg = make_dbg();
   return DPOPT_OK;
 }
 
-int run(void (*kern)(const Act8Params), const Act8Params& p, const char* what,
-        cudaStream_t stream) {
+using Kernel = void (*)(const Act8Params);
+
+int run(Kernel vec, Kernel elem, Act8Params& p, const char* what, cudaStream_t stream) {
   if (p.rows == 0 || p.cols == 0) return DPOPT_OK;
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
-  const int64_t blocks = (p.rows * p.groups + kActThreads - 1) / kActThreads;
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
-  return launched(launch_pdl(kern, grid, kActThreads, 0, stream, p), what);
+  constexpr int kWarps = kActThreads / 32;
+  const int64_t ctas = (p.rows * p.units + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8);
+  const int64_t step = (int64_t)grid * kWarps;
+  p.step_rows = step / p.units;
+  p.step_units = (int)(step % p.units);
+  const bool v = p.cols % 8 == 0 && p.x.vec && p.packed.vec;
+  return launched(launch_pdl(v ? vec : elem, grid, kActThreads, 0, stream, p), what);
 }
 
 }  // namespace
@@ -89,10 +164,12 @@ int dpopt_act8_pack(const void* x, int dtype, int64_t rows, int64_t cols, int64_
   Act8Params p;
   DPOPT_TRY(prepare(p, true, const_cast<void*>(x), dtype, rows, cols, ldx, codes, ld_codes, exps,
                     ld_exps));
-  auto kern = dtype == DPOPT_GRAD_BF16  ? act8_pack_kernel<bf16>
-              : dtype == DPOPT_GRAD_F16 ? act8_pack_kernel<fp16>
-                                        : act8_pack_kernel<float>;
-  return run(kern, p, "act8 pack", (cudaStream_t)stream);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == DPOPT_GRAD_BF16)
+    return run(act8_pack_kernel<bf16, true>, act8_pack_kernel<bf16, false>, p, "act8 pack", st);
+  if (dtype == DPOPT_GRAD_F16)
+    return run(act8_pack_kernel<fp16, true>, act8_pack_kernel<fp16, false>, p, "act8 pack", st);
+  return run(act8_pack_kernel<float, true>, act8_pack_kernel<float, false>, p, "act8 pack", st);
 }
 
 int dpopt_act8_unpack(const int8_t* codes, int64_t ld_codes, const uint8_t* exps, int64_t ld_exps,
@@ -101,10 +178,12 @@ int dpopt_act8_unpack(const int8_t* codes, int64_t ld_codes, const uint8_t* exps
   Act8Params p;
   DPOPT_TRY(prepare(p, false, x, dtype, rows, cols, ldx, const_cast<int8_t*>(codes), ld_codes,
                     const_cast<uint8_t*>(exps), ld_exps));
-  auto kern = dtype == DPOPT_GRAD_BF16  ? act8_unpack_kernel<bf16>
-              : dtype == DPOPT_GRAD_F16 ? act8_unpack_kernel<fp16>
-                                        : act8_unpack_kernel<float>;
-  return run(kern, p, "act8 unpack", (cudaStream_t)stream);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == DPOPT_GRAD_BF16)
+    return run(act8_unpack_kernel<bf16, true>, act8_unpack_kernel<bf16, false>, p, "act8 unpack", st);
+  if (dtype == DPOPT_GRAD_F16)
+    return run(act8_unpack_kernel<fp16, true>, act8_unpack_kernel<fp16, false>, p, "act8 unpack", st);
+  return run(act8_unpack_kernel<float, true>, act8_unpack_kernel<float, false>, p, "act8 unpack", st);
 }
 
 }  // extern "C"

@@ -8,18 +8,19 @@
 namespace dpopt {
 namespace {
 
-// A row is held by a group of tpr threads (a multiple of 32), in NV fragments of 8
-// columns per thread: as few as 512 threads can cover the row with.  In the vector form (VEC: every matrix may be
-// moved 16 bytes at a time) thread t's fragment v is the columns
-// (v tpr + t) 8 .. + 7; in the element form, for odd widths and alignments, its
-// element i is column (v 8 + i) tpr + t, so that a warp always touches
-// neighbouring columns.  Either way a block of 32 columns lies in one warp.
+// A row is held by one CTA of tpr threads (a multiple of 32), in NV fragments of 8
+// columns per thread: as few as 512 threads can cover the row with.  In the
+// vector form (VEC: every matrix may be moved 16 bytes at a time) thread t's
+// fragment v is the columns (v tpr + t) 8 .. + 7; in the element form, for odd
+// widths and alignments, its element i is column (v 8 + i) tpr + t, so that a
+// warp always touches neighbouring columns.  Either way a block of 32 columns
+// lies in one warp.  The row index depends on blockIdx alone, which keeps the
+// row addresses out of the threads' registers.
 constexpr int kJoinCta = 512, kJoinSms = 152;
 
 struct JoinParams {
-  int64_t rows, cols;
-  int tpr, groups;  // threads of a row, rows at a time in a CTA
-  int param_dtype;
+  int64_t rows;
+  int cols, tpr, param_dtype;
   float eps, res_scale, branch_scale;
   int64_t gate_rows;
   Mat h, y, gate, h_out, u;
@@ -35,118 +36,31 @@ __host__ __device__ inline int row_threads(int64_t cols) {
   return (int)((cols + per_warp - 1) / per_warp) * 32;
 }
 
-template <bool VEC>
-__device__ __forceinline__ int column(int v, int i, int t, int tpr) {
-  return VEC ? (v * tpr + t) * 8 + i : (v * 8 + i) * tpr + t;
-}
-
-// Barrier of one row's threads (a whole number of warps).
-__device__ __forceinline__ void group_sync(int group, int tpr) {
-  if (tpr == 32)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-}
-
-// Sum of N values over a row's threads, the same bits in each: the warps'
-// butterflies, then the warps' sums in warp order.  `slot` has a place per warp
-// of the CTA; callers alternate between two such arrays, so that one barrier is
-// enough.
+// Sum of N values over a CTA, the same bits in each thread: the warps'
+// butterflies, then the warps' sums in warp order (or as a butterfly).  Callers
+// alternate between two slot arrays, so that one barrier is enough.
 template <int N>
-__device__ __forceinline__ void group_sum(float (&x)[N], float (*slot)[N], int group, int tpr) {
+__device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
   if (tpr == 32) return;
-  const int warps = tpr >> 5, first = group * warps, lane = threadIdx.x & 31;
+  const int warps = tpr >> 5, lane = threadIdx.x & 31;
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) slot[threadIdx.x >> 5][i] = x[i];
-  group_sync(group, tpr);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (warps <= 4) {
-      x[i] = slot[first][i];
-      for (int w = 1; w < warps; ++w) x[i] += slot[first + w][i];
+      x[i] = slot[0][i];
+      for (int w = 1; w < warps; ++w) x[i] += slot[w][i];
     } else {
-      x[i] = warp_sum(lane < warps ? slot[first + lane][i] : 0.f);
+      const int w = lane & (kJoinCta / 32 - 1);  // both halves of the warp alike
+      x[i] = w < warps ? slot[w][i] : 0.f;
+#pragma unroll
+      for (int o = kJoinCta / 64; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
     }
   }
-}
-
-// One fragment of a matrix in the type it is stored in.
-template <class T, bool VEC>
-struct Frag;
-template <class T>
-struct Frag<T, true> {
-  Raw8<T> r;
-  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
-                                       int64_t cols) {
-    const int c = column<true>(v, 0, t, tpr);
-    r = Raw8<T>{};
-    if (c < cols) r = ld_raw8<T>(static_cast<const T*>(m.data) + row * m.ld + c);
-  }
-  __device__ __forceinline__ void widen(float (&f)[8]) const { widen8<T>(r, f); }
-};
-template <class T>
-struct Frag<T, false> {
-  T e[8];
-  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
-                                       int64_t cols) {
-    const T* p = static_cast<const T*>(m.data) + row * m.ld;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<false>(v, i, t, tpr);
-      e[i] = c < cols ? p[c] : from_f32<T>(0.f);
-    }
-  }
-  __device__ __forceinline__ void widen(float (&f)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
-  }
-};
-
-template <class T, bool VEC>
-__device__ __forceinline__ void frag_store(const Mat& m, int64_t row, int v, int t, int tpr,
-                                           int64_t cols, const float (&f)[8]) {
-  T* p = static_cast<T*>(m.data) + row * m.ld;
-  if constexpr (VEC) {
-    const int c = column<true>(v, 0, t, tpr);
-    if (c < cols) st_vec8<T>(p + c, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<false>(v, i, t, tpr);
-      if (c < cols) p[c] = from_f32<T>(f[i]);
-    }
-  }
-}
-
-// Pack a fragment: in the vector form four threads share a block, in the element
-// form a warp's 32 neighbouring columns are one.  Whole warps call it.
-template <class T, bool VEC>
-__device__ __forceinline__ void frag_pack(const Act8Out& o, int64_t row, int v, int t, int tpr,
-                                          int64_t cols, const float (&f)[8]) {
-  if constexpr (VEC) {
-    act8_store8<T>(o, row, column<true>(v, 0, t, tpr), cols, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<false>(v, i, t, tpr);
-      const uint32_t amax =
-          __reduce_max_sync(0xffffffffu, __float_as_uint(f[i]) & 0x7fffffffu);
-      const uint32_t byte = act8_byte<T>(amax);
-      if (c < cols) {
-        o.codes[row * o.ld_codes + c] = (int8_t)act8_code(f[i], act8_inverse(byte));
-        if ((t & 31) == 0) o.exps[row * o.ld_exps + c / kAct8Block] = (uint8_t)byte;
-      }
-    }
-  }
-}
-
-template <class T>
-__device__ __forceinline__ void round8(const float (&f)[8], float (&r)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = to_f32(from_f32<T>(f[i]));
 }
 
 // Values of a parameter (row `at` elements in; ones where it is absent) at a
@@ -155,7 +69,7 @@ __device__ __forceinline__ void round8(const float (&f)[8], float (&r)[8]) {
 // would take the registers of the loops around it.
 template <bool VEC, int NV>
 __device__ __noinline__ void stage_param(const void* w, int dtype, int64_t at, int t, int tpr,
-                                         int64_t cols, float* out, int stride) {
+                                         int cols, float* out, int stride) {
 #pragma unroll 1
   for (int v = 0; v < NV; ++v)
 #pragma unroll 4
@@ -169,62 +83,61 @@ __device__ __forceinline__ int64_t gate_row_of(int64_t gate_rows, int64_t row) {
   return gate_rows > 0 ? row / gate_rows : 0;
 }
 
-// A group of threads walks rows; the next row's h and y are loaded before the
-// present row's two sums, and h_out stays in registers in fp32 between the norms.
-// The parameters are kept as branch_scale * gate * w_post and w_pre.
+// A CTA walks rows; the next row's h and y are loaded before the present row's
+// two sums, and h_out stays in registers in fp32 between the norms.  The
+// parameters are kept as branch_scale * gate * w_post and w_pre.
 template <class T, bool VEC, int NV>
-__global__ void __launch_bounds__(kJoinCta, 1)
+__global__ void __launch_bounds__(kJoinCta, NV == 1 ? 2 : 1)
     block_join_kernel(const __grid_constant__ JoinParams p) {
   pdl_enter();
   __shared__ float slot[2][kJoinCta / 32][1];
-  const int group = threadIdx.x / p.tpr, t = threadIdx.x - group * p.tpr;
-  const int64_t step = (int64_t)gridDim.x * p.groups;
-  int64_t row = (int64_t)blockIdx.x * p.groups + group;
-  const float inv_c = 1.f / (float)p.cols;
-  int64_t held = -1;  // gate row in pb
-  float pb[NV][8], wpre[NV][8];
   extern __shared__ float stage[];  // 8 NV places per thread
-  float* mine = stage + threadIdx.x;
-  const int stride = blockDim.x;
-  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const int cols = p.cols;
+  if (!dbg_ok(p.dbg, tpr * 8 * NV >= cols)) return;
+  const float inv_c = 1.f / (float)cols;
+  float* mine = stage + t;
+  float pb[NV][8], wpre[NV][8];
+  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, tpr, cols, mine, tpr);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wpre[v][i] = mine[(v * 8 + i) * stride];
+    for (int i = 0; i < 8; ++i) wpre[v][i] = mine[(v * 8 + i) * tpr];
   Frag<T, VEC> fh[NV], fy[NV];
+  int64_t row = blockIdx.x;
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-    if (row < p.rows) {
-      fh[v].load(p.h, row, v, t, p.tpr, p.cols);
-      fy[v].load(p.y, row, v, t, p.tpr, p.cols);
-    }
-  for (; row < p.rows; row += step) {
-    if (!dbg_ok(p.dbg, row >= 0 && p.tpr * 8 * NV >= p.cols)) break;
+  for (int v = 0; v < NV; ++v) {
+    fh[v].load(p.h, row, v, t, tpr, cols);
+    fy[v].load(p.y, row, v, t, tpr, cols);
+  }
+  int64_t held = -1;  // gate row in pb
+  for (; row < p.rows; row += gridDim.x) {
     const int64_t grow = gate_row_of(p.gate_rows, row);
     if (grow != held) {
       held = grow;
-      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, tpr, cols, mine, tpr);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pb[v][i] = p.branch_scale * mine[(v * 8 + i) * stride];
+        for (int i = 0; i < 8; ++i) pb[v][i] = p.branch_scale * mine[(v * 8 + i) * tpr];
       if (p.gate.data) {
-        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, p.tpr, p.cols, mine,
-                             stride);
+        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, tpr, cols, mine,
+                             tpr);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pb[v][i] *= mine[(v * 8 + i) * stride];
+          for (int i = 0; i < 8; ++i) pb[v][i] *= mine[(v * 8 + i) * tpr];
       }
     }
     float h[NV][8], y[NV][8];
+    const int64_t next = row + gridDim.x;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       fh[v].widen(h[v]);
       fy[v].widen(y[v]);
-      if (row + step < p.rows) {
-        fh[v].load(p.h, row + step, v, t, p.tpr, p.cols);
-        fy[v].load(p.y, row + step, v, t, p.tpr, p.cols);
+      if (next < p.rows) {
+        fh[v].load(p.h, next, v, t, tpr, cols);
+        fy[v].load(p.y, next, v, t, tpr, cols);
       }
     }
     float rpost = 1.f;
@@ -234,45 +147,45 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[v][i], y[v][i], ss[0]);
-      group_sum<1>(ss, slot[0], group, p.tpr);
-      rpost = 1.f / sqrtf(fmaf(ss[0], inv_c, p.eps));
+      row_sum<1>(ss, slot[0], tpr);
+      rpost = rsqrtf(fmaf(ss[0], inv_c, p.eps));
       if (t == 0) p.rstd_post[row] = rpost;
     }
     float ss[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      if (p.y8.codes) frag_pack<T, VEC>(p.y8, row, v, t, tpr, cols, y[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         h[v][i] = fmaf(pb[v][i], y[v][i] * rpost, p.res_scale * h[v][i]);
         ss[0] = fmaf(h[v][i], h[v][i], ss[0]);
       }
-      frag_store<T, VEC>(p.h_out, row, v, t, p.tpr, p.cols, h[v]);
-      if (p.y8.codes) frag_pack<T, VEC>(p.y8, row, v, t, p.tpr, p.cols, y[v]);
+      frag_store<T, VEC>(p.h_out, row, v, t, tpr, cols, h[v]);
       if (p.h8.codes) {
         float r[8];
         round8<T>(h[v], r);
-        frag_pack<T, VEC>(p.h8, row, v, t, p.tpr, p.cols, r);
+        frag_pack<T, VEC>(p.h8, row, v, t, tpr, cols, r);
       }
     }
     if (!p.u.data) {
-      group_sync(group, p.tpr);  // the slots of the only sum are used again next row
+      __syncthreads();  // the only sum's slots are used again in the next row
       continue;
     }
-    group_sum<1>(ss, slot[1], group, p.tpr);
-    const float rpre = 1.f / sqrtf(fmaf(ss[0], inv_c, p.eps));
+    row_sum<1>(ss, slot[1], tpr);
+    const float rpre = rsqrtf(fmaf(ss[0], inv_c, p.eps));
     if (t == 0) p.rstd_pre[row] = rpre;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[v][i] *= rpre * wpre[v][i];
-      frag_store<T, VEC>(p.u, row, v, t, p.tpr, p.cols, h[v]);
+      frag_store<T, VEC>(p.u, row, v, t, tpr, cols, h[v]);
       if (p.u8.codes) {
         float r[8];
         round8<T>(h[v], r);
-        frag_pack<T, VEC>(p.u8, row, v, t, p.tpr, p.cols, r);
+        frag_pack<T, VEC>(p.u8, row, v, t, tpr, cols, r);
       }
     }
-    if (!p.rstd_post) group_sync(group, p.tpr);
+    if (!p.rstd_post) __syncthreads();
   }
 }
 
@@ -281,19 +194,19 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 // ---------------------------------------------------------------------------
 
 // Sums over rows: the rows are cut into runs, whose number and borders depend on
-// the sizes alone (as many as 152 SMs hold groups of threads at a time, but no
-// run of fewer than kPartMinRows rows when there are more rows than SMs).  Each run's
-// group leaves one partial row per sum in scratch and the finish kernel adds them
+// the sizes alone (as many as 152 SMs hold CTAs at a time, but no run of fewer
+// than kPartMinRows rows when there are more rows than SMs).  Each run's CTA leaves one partial row per sum in scratch and the finish kernel adds them
 // in order, so the result does not depend on the GPU or on timing.
 constexpr int kPartMinRows = 4;
 
-// Groups of threads a CTA holds at most: a named barrier each.
-__host__ __device__ inline int groups_most(int64_t cols) {
+// CTAs of the gradient's kernel an SM holds (its registers are sized for kJoinCta
+// threads).
+__host__ __device__ inline int ctas_per_sm(int64_t cols) {
   const int n = kJoinCta / row_threads(cols);
-  return n < 1 ? 1 : n < 15 ? n : 15;
+  return n < 1 ? 1 : n;
 }
 __host__ __device__ inline int64_t part_rows(int64_t rows, int64_t cols) {
-  const int64_t at_once = (int64_t)kJoinSms * groups_most(cols);
+  const int64_t at_once = (int64_t)kJoinSms * ctas_per_sm(cols);
   const int64_t each = (rows + at_once - 1) / at_once;
   return each < kPartMinRows && rows > kJoinSms ? kPartMinRows : each < 1 ? 1 : each;
 }
@@ -307,8 +220,8 @@ __host__ __device__ inline int64_t part_count(int64_t rows, int64_t cols) {
 enum { kPartWPre = 0, kPartWPost = 1, kPartGateFirst = 2, kPartGateLast = 3, kPartSlots = 4 };
 
 struct JoinGradParams {
-  int64_t rows, cols, width;  // width: cols rounded up to whole blocks
-  int tpr, groups;
+  int64_t rows, per, parts;  // rows of a part, parts
+  int cols, width, tpr;      // width: cols rounded up to whole blocks
   // the vector form's ring in shared memory: rows held, bytes of one, and where and
   // how large the fragments of each array are (enum kIn*)
   int stages;
@@ -353,13 +266,14 @@ enum { kInDh = 0, kInDu = 1, kInY = 2, kInH = 3 };
 template <class T, bool VEC, int NV>
 struct GradRow {
   const JoinGradParams& p;
-  int t;
-  uint32_t ring;         // this group's ring
-  float scale[2][NV];    // block scales of y and h of the present row
-  uint32_t next[2][NV];  // and the bytes of the next row's
+  const int t, tpr;
+  // this thread's places in a stage of the ring: 16 or 32 bytes a fragment, and 8
+  const uint32_t ring;
+  uint32_t next[2][NV];  // exponent bytes of y and h of the row after the present one
+  float scale[2][NV];    // and the present row's scales
 
-  __device__ __forceinline__ GradRow(const JoinGradParams& q, int t_, uint32_t r)
-      : p(q), t(t_), ring(r) {}
+  __device__ __forceinline__ GradRow(const JoinGradParams& q, uint32_t r)
+      : p(q), t(threadIdx.x), tpr(blockDim.x), ring(r) {}
 
   __device__ __forceinline__ const Mat& mat(int which) const {
     return which == kInDh ? p.dh_out : which == kInDu ? p.du : which == kInY ? p.y : p.h_out;
@@ -373,26 +287,26 @@ struct GradRow {
   __device__ __forceinline__ bool present(int which) const {
     return which == kInDh || which == kInY || p.du.data != nullptr;
   }
-  __device__ __forceinline__ uint32_t slot(int stage, int which, int v) const {
-    return ring + stage * p.stage_bytes + p.frag_at[which] + (v * p.tpr + t) * p.frag_bytes[which];
+  __device__ __forceinline__ uint32_t slot(uint32_t at, int which, int v) const {
+    return at + p.frag_at[which] + (v * tpr + t) * p.frag_bytes[which];
   }
 
-  // Start the copies of a row.
-  __device__ __forceinline__ void fetch(int64_t row, int stage) {
+  // Start the copies of a row into the stage at `at`.
+  __device__ __forceinline__ void fetch(int64_t row, uint32_t at) const {
     if constexpr (VEC) {
 #pragma unroll
       for (int which = 0; which < 4; ++which) {
         if (!present(which)) continue;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const int c = column<true>(v, 0, t, p.tpr);
+          const int c = column<true>(v, 0, t, tpr);
           if (c >= p.cols) continue;
           if (packed(which)) {
-            copy_async8(slot(stage, which, v), act(which).codes + row * act(which).ld_codes + c);
+            copy_async8(slot(at, which, v), act(which).codes + row * act(which).ld_codes + c);
           } else {
             const T* src = static_cast<const T*>(mat(which).data) + row * mat(which).ld + c;
-            copy_async16(slot(stage, which, v), src);
-            if constexpr (sizeof(T) == 4) copy_async16(slot(stage, which, v) + 16, src + 4);
+            copy_async16(slot(at, which, v), src);
+            if constexpr (sizeof(T) == 4) copy_async16(slot(at, which, v) + 16, src + 4);
           }
         }
       }
@@ -403,14 +317,14 @@ struct GradRow {
     if constexpr (VEC) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (packed(kInY + k) && present(kInY + k))
+        if (packed(kInY + k) && present(kInY + k)) {
+          const uint8_t* exps = act(kInY + k).exps + row * act(kInY + k).ld_exps;
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            const int c = column<true>(v, 0, t, p.tpr);
-            next[k][v] = 0;
-            if (c < p.cols)
-              next[k][v] = act(kInY + k).exps[row * act(kInY + k).ld_exps + c / kAct8Block];
+            const int c = column<true>(v, 0, t, tpr);
+            next[k][v] = c < p.cols ? exps[c / kAct8Block] : 0;
           }
+        }
     }
   }
   __device__ __forceinline__ void take_scales() {
@@ -423,15 +337,14 @@ struct GradRow {
     }
   }
 
-  __device__ __forceinline__ void get(int64_t row, int stage, int which, int v,
+  __device__ __forceinline__ void get(int64_t row, uint32_t at, int which, int v,
                                       float (&f)[8]) const {
-    if constexpr (VEC) {
-      if (!present(which) || column<true>(v, 0, t, p.tpr) >= p.cols) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 0.f;
-        return;
-      }
-      const uint32_t a = slot(stage, which, v);
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    if (!present(which)) return;
+    if constexpr (VEC) {
+      if (column<true>(v, 0, t, tpr) >= p.cols) return;
+      const uint32_t a = slot(at, which, v);
       if (packed(which)) {
         uint2 c;
         asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(a) : "memory");
@@ -449,26 +362,20 @@ struct GradRow {
                      : "r"(a + 16)
                      : "memory");
       widen8<T>(r, f);
+    } else if (packed(which)) {
+      const int8_t* codes = act(which).codes + row * act(which).ld_codes;
+      const uint8_t* exps = act(which).exps + row * act(which).ld_exps;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = column<false>(v, i, t, tpr);
+        if (c < p.cols) f[i] = (float)codes[c] * act8_scale(exps[c / kAct8Block]);
+      }
     } else {
+      const T* q = static_cast<const T*>(mat(which).data) + row * mat(which).ld;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-      if (!present(which)) return;
-      if (packed(which)) {
-        const Act8Out& o = act(which);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = column<false>(v, i, t, p.tpr);
-          if (c < p.cols)
-            f[i] = (float)o.codes[row * o.ld_codes + c] *
-                   act8_scale(o.exps[row * o.ld_exps + c / kAct8Block]);
-        }
-      } else {
-        const T* q = static_cast<const T*>(mat(which).data) + row * mat(which).ld;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = column<false>(v, i, t, p.tpr);
-          if (c < p.cols) f[i] = to_f32(q[c]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int c = column<false>(v, i, t, tpr);
+        if (c < p.cols) f[i] = to_f32(q[c]);
       }
     }
   }
@@ -503,44 +410,41 @@ __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t par
     }
 }
 
-// One group of threads per run of rows.  Per row one reading forms three sums,
-//   s = <w_pre du, h>,  a = <q, dh_out + r1 w_pre du>,  b = <q, h>,  q = w_post gate y,
-// from which <w_post dz, y> = branch (a - r1^3 s / C b); a second reading forms
-// the outputs.  Sums over rows per column: dw_pre, and e = sum d y rstd_post,
-// from which, while the gate row stays the same, dw_post grows by branch gate e
-// and dgate is branch w_post e.
+// One CTA per run of rows.  Per row one reading forms three sums,
+//   s = <w_pre du, h>,  a = <q, dh_out + r1 w_pre du>,  b = <q, h>,
+//   q = branch_scale w_post gate y,
+// from which <w_post dz, y> = a - r1^3 s / C b; a second reading forms the outputs.
+// Sums over rows per column: dw_pre, and e = sum d y rstd_post, from which, while
+// the gate row stays the same, dw_post grows by branch gate e and dgate is branch
+// w_post e.
 template <class T, bool VEC, int NV>
 __global__ void __launch_bounds__(kJoinCta, 1)
     block_join_grad_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float slot[2][kJoinCta / 32][3];
-  const int group = threadIdx.x / p.tpr, t = threadIdx.x - group * p.tpr;
-  const int64_t parts = part_count(p.rows, p.cols), per = part_rows(p.rows, p.cols);
-  const int64_t part = (int64_t)blockIdx.x * p.groups + group;
-  if (part >= parts || !dbg_ok(p.dbg, p.tpr * 8 * NV >= p.cols)) return;
-  const int64_t lo = part * per, hi = min(p.rows, lo + per);
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const int64_t lo = blockIdx.x * p.per, hi = min(p.rows, lo + p.per);
+  if (!dbg_ok(p.dbg, tpr * 8 * NV >= p.cols && lo < hi)) return;
   const float inv_c = 1.f / (float)p.cols;
-  // dw_post of finished gate rows, one place per column of a thread
-  const int stride = blockDim.x;
-  float* post = reinterpret_cast<float*>(dyn) + threadIdx.x;
-  float* mine = post + 8 * NV * stride;  // parameters and sums on their way
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dyn) +
-                        16 * NV * stride * (uint32_t)sizeof(float) +
-                        group * p.stages * p.stage_bytes;
-  GradRow<T, VEC, NV> in(p, t, ring);
+  // dw_post of finished gate rows, and parameters and sums on their way: one
+  // place per column of a thread
+  float* post = reinterpret_cast<float*>(dyn) + t;
+  float* mine = post + 8 * NV * tpr;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dyn) + 16 * NV * tpr * 4;
+  GradRow<T, VEC, NV> in(p, ring);
   float wpre[NV][8], q[NV][8], acc[NV][8], e[NV][8];
-  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      wpre[v][i] = mine[(v * 8 + i) * stride];
+      wpre[v][i] = mine[(v * 8 + i) * tpr];
       acc[v][i] = e[v][i] = 0.f;
-      post[(v * 8 + i) * stride] = 0.f;
+      post[(v * 8 + i) * tpr] = 0.f;
     }
   for (int s = 0; s < p.stages; ++s) {
-    if (lo + s < hi) in.fetch(lo + s, s);
+    if (lo + s < hi) in.fetch(lo + s, ring + s * p.stage_bytes);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   in.fetch_scales(lo);
@@ -551,24 +455,25 @@ __global__ void __launch_bounds__(kJoinCta, 1)
     const int64_t grow = gate_row_of(p.gate_rows, row);
     if (grow != held) {
       held = grow;
-      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, p.tpr, p.cols, mine, stride);
+      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[v][i] = mine[(v * 8 + i) * stride];
+        for (int i = 0; i < 8; ++i) q[v][i] = p.branch_scale * mine[(v * 8 + i) * tpr];
       if (p.gate.data) {
-        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, p.tpr, p.cols, mine,
-                             stride);
+        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, tpr, p.cols, mine,
+                             tpr);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[v][i] *= mine[(v * 8 + i) * stride];
+          for (int i = 0; i < 8; ++i) q[v][i] *= mine[(v * 8 + i) * tpr];
       }
     }
     const float r1 = p.du.data ? p.rstd_pre[row] : 0.f;
     const float r2 = p.rstd_post ? p.rstd_post[row] : 1.f;
     in.take_scales();
     if (row + 1 < hi) in.fetch_scales(row + 1);
+    const uint32_t at = ring + stage * p.stage_bytes;
     if constexpr (VEC) {
       // the oldest of the rows asked for has arrived
       if (p.stages == 1)
@@ -578,17 +483,17 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       else
         asm volatile("cp.async.wait_group 2;" ::: "memory");
     }
-    float sum[3] = {0.f, 0.f, 0.f};
+    float sum[3];
     {
       uint64_t s2 = 0, a2 = 0, b2 = 0;
       const uint64_t rr = pair(r1, r1);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float d[8], u[8], h[8], y[8];
-        in.get(row, stage, kInDh, v, d);
-        in.get(row, stage, kInDu, v, u);
-        in.get(row, stage, kInY, v, y);
-        in.get(row, stage, kInH, v, h);
+        in.get(row, at, kInDh, v, d);
+        in.get(row, at, kInDu, v, u);
+        in.get(row, at, kInY, v, y);
+        in.get(row, at, kInH, v, h);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint64_t wu = mul2(pair(wpre[v][i], wpre[v][i + 1]), pair(u[i], u[i + 1]));
@@ -603,50 +508,51 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       sum[1] = lane0(a2) + lane1(a2);
       sum[2] = lane0(b2) + lane1(b2);
     }
-    group_sum<3>(sum, slot[row & 1], group, p.tpr);
+    row_sum<3>(sum, slot[row & 1], tpr);
     const float k1 = r1 * r1 * r1 * sum[0] * inv_c;
-    const float k2 = p.rstd_post
-                         ? r2 * r2 * r2 * p.branch_scale * (sum[1] - k1 * sum[2]) * inv_c
-                         : 0.f;
-    const float c1 = r2 * p.branch_scale;
+    const float k2 = p.rstd_post ? r2 * r2 * r2 * (sum[1] - k1 * sum[2]) * inv_c : 0.f;
     {
       const uint64_t r1p = pair(r1, r1), r2p = pair(r2, r2), k1p = pair(-k1, -k1),
-                     k2p = pair(-k2, -k2), c1p = pair(c1, c1),
-                     resp = pair(p.res_scale, p.res_scale);
+                     k2p = pair(-k2, -k2);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float d[8], u[8], h[8], y[8];
-        in.get(row, stage, kInDh, v, d);
-        in.get(row, stage, kInDu, v, u);
-        in.get(row, stage, kInY, v, y);
-        in.get(row, stage, kInH, v, h);
+        in.get(row, at, kInDh, v, d);
+        in.get(row, at, kInDu, v, u);
+        in.get(row, at, kInY, v, y);
+        in.get(row, at, kInH, v, h);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint64_t u2 = pair(u[i], u[i + 1]), y2 = pair(y[i], y[i + 1]);
           const uint64_t h2 = pair(h[i], h[i + 1]);
-          const uint64_t lin = fma2(r1p, mul2(pair(wpre[v][i], wpre[v][i + 1]), u2),
-                                    pair(d[i], d[i + 1]));
-          const uint64_t full = fma2(k1p, h2, lin);
+          const uint64_t full =
+              fma2(k1p, h2, fma2(r1p, mul2(pair(wpre[v][i], wpre[v][i + 1]), u2),
+                                 pair(d[i], d[i + 1])));
+          const uint64_t fr = mul2(full, r2p);
           const uint64_t ac = fma2(u2, mul2(h2, r1p), pair(acc[v][i], acc[v][i + 1]));
-          const uint64_t ee = fma2(full, mul2(y2, r2p), pair(e[v][i], e[v][i + 1]));
-          const uint64_t dh = mul2(full, resp);
-          const uint64_t dy =
-              fma2(k2p, y2, mul2(pair(q[v][i], q[v][i + 1]), mul2(full, c1p)));
+          const uint64_t ee = fma2(fr, y2, pair(e[v][i], e[v][i + 1]));
+          const uint64_t dy = fma2(k2p, y2, mul2(pair(q[v][i], q[v][i + 1]), fr));
           acc[v][i] = lane0(ac);
           acc[v][i + 1] = lane1(ac);
           e[v][i] = lane0(ee);
           e[v][i + 1] = lane1(ee);
-          d[i] = lane0(dh);
-          d[i + 1] = lane1(dh);
+          d[i] = lane0(full);
+          d[i + 1] = lane1(full);
           u[i] = lane0(dy);
           u[i + 1] = lane1(dy);
         }
-        if (p.dh.data) frag_store<T, VEC>(p.dh, row, v, t, p.tpr, p.cols, d);
-        frag_store<T, VEC>(p.dy, row, v, t, p.tpr, p.cols, u);
+        if (p.dh.data) {
+          if (p.res_scale != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= p.res_scale;
+          }
+          frag_store<T, VEC>(p.dh, row, v, t, tpr, p.cols, d);
+        }
+        frag_store<T, VEC>(p.dy, row, v, t, tpr, p.cols, u);
       }
     }
     if constexpr (VEC) {
-      if (row + p.stages < hi) in.fetch(row + p.stages, stage);
+      if (row + p.stages < hi) in.fetch(row + p.stages, at);
       asm volatile("cp.async.commit_group;" ::: "memory");
       stage = stage + 1 == p.stages ? 0 : stage + 1;
     }
@@ -656,10 +562,10 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          mine[(v * 8 + i) * stride] = p.branch_scale * e[v][i];
+          mine[(v * 8 + i) * tpr] = p.branch_scale * e[v][i];
           e[v][i] = 0.f;
         }
-      close_gate_row<VEC, NV>(p, part, lo, hi, row, first_gate, t, post, mine, stride);
+      close_gate_row<VEC, NV>(p, blockIdx.x, lo, hi, row, first_gate, t, post, mine, tpr);
       first_gate = false;
     }
   }
@@ -667,10 +573,10 @@ __global__ void __launch_bounds__(kJoinCta, 1)
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(v, i, t, p.tpr);
+      const int c = column<VEC>(v, i, t, tpr);
       if (c >= p.cols) continue;
-      if (p.dw_pre) part_row(p, part, kPartWPre)[c] = acc[v][i];
-      if (p.dw_post) part_row(p, part, kPartWPost)[c] = post[(v * 8 + i) * stride];
+      if (p.dw_pre) part_row(p, blockIdx.x, kPartWPre)[c] = acc[v][i];
+      if (p.dw_post) part_row(p, blockIdx.x, kPartWPost)[c] = post[(v * 8 + i) * tpr];
     }
 }
 
@@ -684,7 +590,7 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
 block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   __shared__ float run_sum[kFinishRuns][33];
-  const int64_t parts = part_count(p.rows, p.cols), per = part_rows(p.rows, p.cols);
+  const int64_t parts = p.parts, per = p.per;
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   int slot = blockIdx.y;
@@ -760,12 +666,6 @@ int64_t whole_blocks(int64_t cols) {
   return (cols + kAct8Block - 1) / kAct8Block * kAct8Block;
 }
 
-// Rows (or runs of rows) at a time in a CTA: at most `most`, and fewer when there
-// are too few to give every SM a CTA.
-int group_count(int most, int64_t rows) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (rows + kJoinSms - 1) / kJoinSms));
-}
-
 bool vec_ok(const Mat& m) { return !m.data || m.vec; }
 bool vec_ok(const Act8Out& a) { return !a.codes || a.vec; }
 
@@ -784,15 +684,13 @@ int launch_join_at(JoinParams& p, cudaStream_t stream) {
   auto kern = block_join_kernel<T, VEC, NV>;
   int sms = 0, per_sm = 0;
   DPOPT_TRY(sm_count(&sms));
-  p.groups = group_count(std::max(1, std::min(15, 256 / p.tpr)), p.rows);
-  const int threads = p.groups * p.tpr;
-  const size_t smem = (size_t)threads * 8 * NV * sizeof(float);
+  const size_t smem = (size_t)p.tpr * 8 * NV * sizeof(float);
   DPOPT_TRY(allow_smem(kern, smem));
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.tpr, smem);
   if (e != cudaSuccess) return cuda_fail(e, "block join occupancy");
-  const int64_t ctas = (p.rows + p.groups - 1) / p.groups;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * std::max(per_sm, 1));
-  return launched(launch_pdl(kern, grid, threads, smem, stream, p), "block join");
+  const unsigned grid =
+      (unsigned)std::min<int64_t>(p.rows, (int64_t)sms * std::max(per_sm, 1));
+  return launched(launch_pdl(kern, grid, p.tpr, smem, stream, p), "block join");
 }
 
 template <class T>
@@ -810,21 +708,18 @@ int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
 template <class T, bool VEC, int NV>
 int launch_join_grad_at(JoinGradParams& p, cudaStream_t stream) {
   auto kern = block_join_grad_kernel<T, VEC, NV>;
-  const int64_t parts = part_count(p.rows, p.cols);
-  p.groups = group_count(groups_most(p.cols), parts);
-  const int threads = p.groups * p.tpr;
-  const size_t post = (size_t)threads * 16 * NV * sizeof(float);
-  const size_t row = (size_t)p.stage_bytes * p.groups;
-  p.stages = VEC ? (int)std::min<size_t>(3, (kJoinSmem - post) / row) : 0;
-  const size_t smem = post + p.stages * row;
+  const size_t room = kJoinSmem / ctas_per_sm(p.cols);
+  const size_t sums = (size_t)p.tpr * 16 * NV * sizeof(float);
+  p.stages = VEC ? (int)std::min<size_t>(3, (room - sums) / p.stage_bytes) : 0;
+  const size_t smem = sums + (size_t)p.stages * p.stage_bytes;
   DPOPT_TRY(allow_smem(kern, smem));
-  const unsigned grid = (unsigned)((parts + p.groups - 1) / p.groups);
-  return launched(launch_pdl(kern, grid, threads, smem, stream, p), "block join gradient");
+  return launched(launch_pdl(kern, (unsigned)p.parts, p.tpr, smem, stream, p),
+                  "block join gradient");
 }
 
 template <class T>
 int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
-  const int nv = row_frags(p.cols), groups = groups_most(p.cols);
+  const int nv = row_frags(p.cols);
   p.stage_bytes = 0;
   for (int which = 0; which < 4; ++which) {
     const bool packed = (which == kInY && p.y8.codes) || (which == kInH && p.h8.codes);
@@ -834,7 +729,7 @@ int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
       p.stage_bytes += p.frag_bytes[which] * nv * p.tpr;
   }
   // the vector form needs room for at least one row of the ring
-  vec = vec && (size_t)groups * (p.tpr * 16 * nv * sizeof(float) + p.stage_bytes) <= kJoinSmem;
+  vec = vec && p.tpr * 16 * nv * sizeof(float) + p.stage_bytes <= kJoinSmem / ctas_per_sm(p.cols);
   switch (nv) {
     case 1:
       return vec ? launch_join_grad_at<T, true, 1>(p, stream)
@@ -895,7 +790,7 @@ int dpopt_block_join(const dpopt_block_join_args* a, dpopt_stream_t stream) {
   if (a->u8.codes) DPOPT_TRY(take_act8("u8", a->u8, rows, cols, true, &p.u8, s, &n));
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
-  p.cols = cols;
+  p.cols = (int)cols;
   p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.eps = a->eps;
@@ -993,7 +888,7 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   }
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
-  p.cols = cols;
+  p.cols = (int)cols;
   p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.res_scale = a->res_scale;
@@ -1008,7 +903,9 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   p.partial = static_cast<float*>(a->scratch);
   p.dbg = make_dbg();
   const int64_t parts = part_count(rows, cols);
-  p.width = whole_blocks(cols);
+  p.width = (int)whole_blocks(cols);
+  p.per = part_rows(rows, cols);
+  p.parts = parts;
   if (rows > 0) {
     const bool vec = cols % 8 == 0 && vec_ok(p.dh_out) && vec_ok(p.du) && vec_ok(p.y) &&
                      vec_ok(p.h_out) && vec_ok(p.dh) && vec_ok(p.dy) && vec_ok(p.y8) &&

@@ -198,35 +198,52 @@ struct Act8Out {
   int vec;  // codes may be moved 8 at a time
 };
 
-// Pack the eight values f of columns col.. of one row.  The four threads of a
-// block's 32 columns (adjacent lanes, the first at a multiple of four) call it
-// together; columns from `cols` on carry zeros and are not stored.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Pack the eight values f of columns col.. of one row, all of them or none below
+// cols.  The four threads of a block's 32 columns (adjacent lanes, the first at a
+// multiple of four) call it together; columns from `cols` on carry zeros and are
+// not stored.
 template <class T>
-__device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int64_t col,
-                                            int64_t cols, const float (&f)[8]) {
-  uint32_t amax = 0;
+__device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int col, int cols,
+                                            const float (&f)[8]) {
+  float m = fabsf(f[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(f[i]) & 0x7fffffffu);
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t amax = __float_as_uint(m);
   const uint32_t byte = act8_byte<T>(amax);
   const float inv = act8_inverse(byte);
-  int8_t* dst = o.codes + row * o.ld_codes + col;
-  if (o.vec && col + 8 <= cols) {
-    uint32_t lo = 0, hi = 0;
+  uint32_t lo, hi;
+  if ((amax & 0x7fffffu) >= 0x7f0000u || byte == 255u) {
+    // a value may round to 128 and is clamped (the block's largest is 127.5 steps or
+    // more), or the block is not finite
+    lo = hi = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lo |= act8_code(f[i], inv) << (8 * i);
       hi |= act8_code(f[4 + i], inv) << (8 * i);
     }
-    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
   } else {
+    const uint64_t i2 = pair(inv, inv), m2 = pair(12582912.f, 12582912.f);
+    uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) dst[i] = (int8_t)act8_code(f[i], inv);
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t v = fma2(pair(f[i], f[i + 1]), i2, m2);  // the product is exact
+      c[i] = (uint32_t)v;
+      c[i + 1] = (uint32_t)(v >> 32);
+    }
+    lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
   }
-  if (col < cols && (threadIdx.x & 3) == 0)
-    o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
+  if (col >= cols) return;
+  *reinterpret_cast<uint2*>(o.codes + row * o.ld_codes + col) = make_uint2(lo, hi);
+  if ((threadIdx.x & 3) == 0) o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
 }
 
 // Eight codes (two words) times a scale.  A code with its sign bit turned over is
@@ -247,19 +264,6 @@ __device__ __forceinline__ void act8_values(uint2 c, float scale, float (&f)[8])
   }
 }
 
-// Values of columns col.. of one row (zeros from `cols` on).
-__device__ __forceinline__ void act8_load8(const Act8Out& o, int64_t row, int64_t col,
-                                           int64_t cols, float (&f)[8]) {
-  const int8_t* src = o.codes + row * o.ld_codes + col;
-  const float scale = col < cols ? act8_scale(o.exps[row * o.ld_exps + col / kAct8Block]) : 0.f;
-  if (o.vec && col + 8 <= cols) {
-    act8_values(*reinterpret_cast<const uint2*>(src), scale, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? (float)src[i] * scale : 0.f;
-  }
-}
-
 // A matrix a kernel reads or writes (data null: absent).
 struct Mat {
   void* data;
@@ -267,29 +271,89 @@ struct Mat {
   int vec;  // rows may be moved 8 elements at a time
 };
 
+// Columns of a thread's fragment v of 8: in the vector form (VEC: the matrices may
+// be moved 8 elements at a time) adjacent ones, in the element form one from each
+// of 8 runs of tpr, so that a warp always touches neighbouring columns.  tpr is a
+// multiple of 32; either way a block of 32 columns lies in one warp.
+template <bool VEC>
+__device__ __forceinline__ int column(int v, int i, int t, int tpr) {
+  return VEC ? (v * tpr + t) * 8 + i : (v * 8 + i) * tpr + t;
+}
+
+// One fragment of a matrix in the type it is stored in.
+template <class T, bool VEC>
+struct Frag;
 template <class T>
-__device__ __forceinline__ void mat_load8(const Mat& m, int64_t row, int64_t col, int64_t cols,
-                                          float (&f)[8]) {
-  const T* src = static_cast<const T*>(m.data) + row * m.ld + col;
-  if (m.vec && col + 8 <= cols) {
-    widen8<T>(ld_raw8<T>(src), f);
+struct Frag<T, true> {
+  Raw8<T> r;
+  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
+                                       int cols, int c0 = 0) {
+    const int c = c0 + column<true>(v, 0, t, tpr);
+    r = Raw8<T>{};
+    if (c < cols) r = ld_raw8<T>(static_cast<const T*>(m.data) + row * m.ld + c);
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const { widen8<T>(r, f); }
+};
+template <class T>
+struct Frag<T, false> {
+  T e[8];
+  __device__ __forceinline__ void load(const Mat& m, int64_t row, int v, int t, int tpr,
+                                       int cols, int c0 = 0) {
+    const T* p = static_cast<const T*>(m.data) + row * m.ld;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + column<false>(v, i, t, tpr);
+      e[i] = c < cols ? p[c] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
+  }
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void frag_store(const Mat& m, int64_t row, int v, int t, int tpr,
+                                           int cols, const float (&f)[8], int c0 = 0) {
+  T* p = static_cast<T*>(m.data) + row * m.ld;
+  if constexpr (VEC) {
+    const int c = c0 + column<true>(v, 0, t, tpr);
+    if (c < cols) st_vec8<T>(p + c, f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? to_f32(src[i]) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + column<false>(v, i, t, tpr);
+      if (c < cols) p[c] = from_f32<T>(f[i]);
+    }
+  }
+}
+
+// Pack a fragment: in the vector form four threads share a block, in the element
+// form a warp's 32 neighbouring columns are one.  Whole warps call it.
+template <class T, bool VEC>
+__device__ __forceinline__ void frag_pack(const Act8Out& o, int64_t row, int v, int t, int tpr,
+                                          int cols, const float (&f)[8], int c0 = 0) {
+  if constexpr (VEC) {
+    act8_store8<T>(o, row, c0 + column<true>(v, 0, t, tpr), cols, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + column<false>(v, i, t, tpr);
+      const uint32_t amax =
+          __reduce_max_sync(0xffffffffu, __float_as_uint(f[i]) & 0x7fffffffu);
+      const uint32_t byte = act8_byte<T>(amax);
+      if (c < cols) {
+        o.codes[row * o.ld_codes + c] = (int8_t)act8_code(f[i], act8_inverse(byte));
+        if ((t & 31) == 0) o.exps[row * o.ld_exps + c / kAct8Block] = (uint8_t)byte;
+      }
+    }
   }
 }
 
 template <class T>
-__device__ __forceinline__ void mat_store8(const Mat& m, int64_t row, int64_t col, int64_t cols,
-                                           const float (&f)[8]) {
-  T* dst = static_cast<T*>(m.data) + row * m.ld + col;
-  if (m.vec && col + 8 <= cols) {
-    st_vec8<T>(dst, f);
-  } else {
+__device__ __forceinline__ void round8(const float (&f)[8], float (&r)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) dst[i] = from_f32<T>(f[i]);
-  }
+  for (int i = 0; i < 8; ++i) r[i] = to_f32(from_f32<T>(f[i]));
 }
 
 // ---------------------------------------------------------------------------

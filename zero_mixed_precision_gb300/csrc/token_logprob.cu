@@ -44,11 +44,6 @@ struct LogprobParams {
   Dbg dbg;
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // 2^x to two units in the last place; results below 2^-126 are 0 (keeping them
 // would cost three more instructions for each logit).
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -453,7 +448,7 @@ struct LogprobGradParams {
 constexpr int64_t kGradStretch = 4 * kTokThreads * 8;
 
 template <class T>
-__global__ void __launch_bounds__(kTokThreads)
+__global__ void __launch_bounds__(kTokThreads, 4)
 token_logprob_grad_kernel(const LogprobGradParams p) {
   pdl_enter();
   __shared__ int64_t tok[DPOPT_MAX_TOKENS];
@@ -464,6 +459,14 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
   const int64_t hi = min(p.vocab, lo + p.stretch_len);
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
   T* out = static_cast<T*>(p.dlogits) + row * p.ld_out;
+  const Stretch<T> st(x, lo, hi);
+  const T* body = st.x + st.head;
+  // most stretches are four vectors a thread: ask for them before anything else
+  const bool whole = st.vecs >= 4 * kTokThreads;
+  Raw8<T> r[4];
+  if (whole)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = ld_raw8<T>(body + (threadIdx.x + u * kTokThreads) * 8);
   const float scale = (p.loss_scale ? p.loss_scale->scale : 1.f) * p.inv_temp;
   const float m = p.stats[row * 2], logsum = p.stats[row * 2 + 1];
   const float dh = p.dentropy ? p.dentropy[row] : 0.f;
@@ -486,7 +489,6 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
   const bool zero = m == -INFINITY || (none && dh == 0.f);
   const float l2 = logsum * kLog2e;
   const float A = -scale * fmaf(dh, ent, a), B = -scale * dh * kLn2;
-  const Stretch<T> st(x, lo, hi);
   T* dst = out + lo;
   auto grad = [&](float v) {
     const float q = max_nan(fmaf(v - m, p.c, -l2), -1e4f);
@@ -497,7 +499,6 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
     dst[j] = from_f32<T>(grad(to_f32(st.x[j])));
   }
   const bool vec = ((uintptr_t)(dst + st.head) & 15) == 0;
-  const T* body = st.x + st.head;
   auto eight = [&](const Raw8<T>& r, int64_t v) {
     float f[8];
     widen8<T>(r, f);
@@ -533,12 +534,10 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
     return;
   }
   int64_t v = threadIdx.x;
-  for (; v + 3 * kTokThreads < st.vecs; v += 4 * kTokThreads) {
-    Raw8<T> r[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) r[u] = ld_raw8<T>(body + (v + u * kTokThreads) * 8);
+  if (whole) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) eight(r[u], v + u * kTokThreads);
+    v += 4 * kTokThreads;
   }
   for (; v < st.vecs; v += kTokThreads) eight(ld_raw8<T>(body + v * 8), v);
   __syncthreads();
