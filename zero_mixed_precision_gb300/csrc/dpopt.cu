@@ -1444,9 +1444,12 @@ int dpopt_stream_status(dpopt_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
   bool timed_out = false;
-  const int rc = take_wait_status(&timed_out);
+  int rc = take_wait_status(&timed_out);
   if (rc) return rc;
-  if (timed_out) return DPOPT_ERR_TIMEOUT;
+  bool gemm_timed_out = false;
+  rc = take_gemm_status(&gemm_timed_out);
+  if (rc) return rc;
+  if (timed_out || gemm_timed_out) return DPOPT_ERR_TIMEOUT;
 #ifdef DPOPT_DEBUG_BOUNDS
   unsigned int word = 0;
   e = cudaMemcpyFromSymbol(&word, g_bounds_status, sizeof word);

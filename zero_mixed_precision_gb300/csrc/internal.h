@@ -103,6 +103,8 @@ int run_tma(const SegDesc* segs, int s0, int s1, int n, int grad_dtype, float* m
 // Reads and clears the sticky status word of the bounded waits: *timed_out
 // is set when a wait gave up since the last call.
 int take_wait_status(bool* timed_out);
+// The same for the waits of the weight-gradient product (act8_wgrad.cu).
+int take_gemm_status(bool* timed_out);
 // The bounded-wait self-test launch (a wait on a barrier nothing completes).
 int launch_selftest_wait(long long limit_cycles, cudaStream_t stream);
 // Longest bounded wait, in clock cycles (about one second).

@@ -423,9 +423,9 @@ inline int check_overlaps(const Span* s, int n) {
   return DPOPT_OK;
 }
 
-#define DPOPT_TRY(expr)                      \
+#define DPOPT_TRY(...)                       \
   do {                                       \
-    const int try_rc_ = (expr);              \
+    const int try_rc_ = (__VA_ARGS__);       \
     if (try_rc_ != DPOPT_OK) return try_rc_; \
   } while (0)
 
