@@ -85,8 +85,12 @@ __global__ void __launch_bounds__(kOperandThreads)
 // the product
 // ---------------------------------------------------------------------------
 
-// A CTA owns a tile of kTileM rows of dw (columns of dy) by BN columns (of the
-// input) and steps over kStep tokens at a time.
+// CG CTAs (one, or a pair that shares its products' operands) own a tile of
+// CG x kTileM rows of dw (columns of dy) by BN columns (of the input) and step over
+// kStep tokens at a time.  In a pair each CTA copies its own 128 rows and half of
+// the BN columns, the first CTA issues products of 256 rows that read both CTAs'
+// shared memory, and each CTA's tensor memory receives its own rows: per step a
+// CTA copies 32 KB, for four times the products of a 128 x 128 tile's 32 KB.
 constexpr int kTileM = 128, kStep = 64;
 constexpr int kBoxBytes = 64 * kStep * 2;  // one copied box: 64 columns x kStep tokens
 constexpr int kGemmThreads = 192;          // copying warp, issuing warp, four epilogue warps
@@ -104,11 +108,11 @@ struct GemmParams {
   Dbg dbg;
 };
 
-template <int BN>
+template <int CG, int BN>
 struct GemmShape {
-  static constexpr int kBoxes = kTileM / 64 + BN / 64;
-  static constexpr int kStageBytes = kBoxes * kBoxBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kBoxesA = kTileM / 64, kBoxesB = BN / CG / 64;
+  static constexpr int kStageBytes = (kBoxesA + kBoxesB) * kBoxBytes;
+  static constexpr int kStages = 6;
   static constexpr int kSmem = kStages * kStageBytes + 1024;  // 1024-byte aligned
 };
 
@@ -132,13 +136,34 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, long lo
   return true;
 }
 
+// Copies one box to this CTA's shared memory; `bar`, which counts its bytes, may be
+// the pair's first CTA's.
+template <int CG>
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y,
                                         uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// The address of a shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Shared-memory matrix descriptor of a 16-bit operand whose 64-element runs along
@@ -150,27 +175,66 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 }
 
 // Instruction descriptor: fp32 accumulators, operands of type T, both with the
-// token index slow (transposed), a kTileM x BN tile.
-template <class T, int BN>
+// token index slow (transposed), a CG kTileM x BN tile.
+template <class T, int CG, int BN>
 __device__ __forceinline__ constexpr uint32_t instr_desc() {
   constexpr uint32_t fmt = std::is_same_v<T, bf16> ? 1u : 0u;
   return 1u << 4 | fmt << 7 | fmt << 10 | 1u << 15 | 1u << 16 | (uint32_t)(BN / 8) << 17 |
-         (uint32_t)(kTileM / 16) << 24;
+         (uint32_t)(CG * kTileM / 16) << 24;
 }
 
+template <int CG>
 __device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
 }
 
+// Arrives on `bar`, in both CTAs of a pair, when the products issued so far are done.
+template <int CG>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
@@ -193,7 +257,7 @@ struct Unit {
   int64_t t0;
 };
 
-template <int BN>
+template <int CG, int BN>
 __device__ __forceinline__ Unit unit_at(const GemmParams& p, int u) {
   const int tiles = p.tiles_m * p.tiles_n;
   Unit r;
@@ -203,7 +267,7 @@ __device__ __forceinline__ Unit unit_at(const GemmParams& p, int u) {
   const int first = group * kTileGroup;
   const int rows = min(kTileGroup, p.tiles_m - first);
   const int local = tile - group * kTileGroup * p.tiles_n;
-  r.m0 = (first + local % rows) * kTileM;
+  r.m0 = (first + local % rows) * CG * kTileM;
   r.n0 = (local / rows) * BN;
   r.t0 = r.split * p.per_split;
   const int64_t t1 = min(p.tokens, r.t0 + p.per_split);
@@ -211,12 +275,33 @@ __device__ __forceinline__ Unit unit_at(const GemmParams& p, int u) {
   return r;
 }
 
-// 32 columns of one row of a tile: to the partial sums, or with the addend to dw.
-template <int BN>
-__device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int row, int col,
-                                        const uint32_t (&r)[32]) {
-  if (row >= p.n || col >= p.k || !dbg_ok(p.dbg, row >= 0 && col >= 0)) return;
+// Rows row0 .. + rows of column c, the sums at x[33 i]: the addend's values are all
+// asked for before the first store.
+template <class T>
+__device__ __forceinline__ void store_columns(const GemmParams& p, int row0, int c, int rows,
+                                              const float* x) {
+  T add[32];
+  if (p.addend.data) {
+    const T* a = static_cast<const T*>(p.addend.data) + row0 * p.addend.ld + c;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) add[i] = i < rows ? a[i * p.addend.ld] : from_f32<T>(0.f);
+  }
+  T* d = static_cast<T*>(p.dw.data) + row0 * p.dw.ld + c;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < rows)
+      d[i * p.dw.ld] = from_f32<T>(p.addend.data ? x[33 * i] + to_f32(add[i]) : x[33 * i]);
+}
+
+// 32 rows x 32 columns of a tile, a row per lane, from a warp's registers to memory.
+// Partial sums, and results without an addend whose rows are 16-byte aligned, go
+// out as vectors, a row's 32 columns per lane; others go through shared memory
+// (`swap`, 32 x 33) so that a warp's loads and stores touch neighbouring columns.
+__device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int row0, int col,
+                                        const uint32_t (&r)[32], float* swap) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
   if (p.splits > 1) {
+    if (row >= p.n || !dbg_ok(p.dbg, col < p.pk)) return;
     float* dst = p.partial + ((int64_t)u.split * p.n + row) * p.pk + col;
 #pragma unroll
     for (int i = 0; i < 32; i += 4)
@@ -224,23 +309,14 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int 
         *reinterpret_cast<uint4*>(dst + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
     return;
   }
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-  const bool whole = col + 32 <= p.k;
-  if (p.addend.data) {
-    const int64_t at = row * p.addend.ld + col;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (whole || col + i < p.k) f[i] += ld_any(p.addend.data, p.out_dtype, at + i);
-  }
-  const int64_t at = row * p.dw.ld + col;
-  if (whole && p.dw.vec) {
+  if (p.dw.vec && !p.addend.data && col + 32 <= p.k) {
+    if (row >= p.n) return;
+    const int64_t at = row * p.dw.ld + col;
     if (p.out_dtype == DPOPT_GRAD_F32) {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.dw.data) + at);
+      uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(p.dw.data) + at);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        d[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
     } else {
       uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw.data) + at);
       const bool b = p.out_dtype == DPOPT_GRAD_BF16;
@@ -248,34 +324,50 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int 
       for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = b ? pack2(f[8 * i + 2 * j], f[8 * i + 2 * j + 1], bf16())
-                   : pack2(f[8 * i + 2 * j], f[8 * i + 2 * j + 1], fp16());
+        for (int j = 0; j < 4; ++j) {
+          const float x = __uint_as_float(r[8 * i + 2 * j]);
+          const float y = __uint_as_float(r[8 * i + 2 * j + 1]);
+          w[j] = b ? pack2(x, y, bf16()) : pack2(x, y, fp16());
+        }
         d[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < p.k) st_any(p.dw.data, p.out_dtype, at + i, f[i]);
+    return;
   }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) swap[lane * 33 + i] = __uint_as_float(r[i]);
+  __syncwarp();
+  const int c = col + lane, rows = min(32, p.n - row0);
+  if (c >= p.k || rows <= 0) return;
+  if (p.out_dtype == DPOPT_GRAD_F32)
+    store_columns<float>(p, row0, c, rows, swap + lane);
+  else if (p.out_dtype == DPOPT_GRAD_BF16)
+    store_columns<bf16>(p, row0, c, rows, swap + lane);
+  else
+    store_columns<fp16>(p, row0, c, rows, swap + lane);
 }
 
-// One warp copies boxes into a ring of stages, one issues the products of a stage
-// (four of 16 tokens), four bring finished tiles from tensor memory to memory;
-// two accumulators let the next tile's products run under a tile's epilogue.
-template <class T, int BN>
+// One warp copies boxes into a ring of stages, one (of a pair's first CTA) issues
+// the products of a stage (four of 16 tokens), four bring finished tiles from
+// tensor memory to memory; two accumulators let the next tile's products run
+// under a tile's epilogue.  In a pair the first CTA's `full` counts both CTAs'
+// bytes and its `taken` both CTAs' epilogue warps; `empty` and `done` are arrived
+// on in both.
+template <class T, int CG, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     act8_wgrad_kernel(const __grid_constant__ GemmParams p,
                       const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b) {
-  using S = GemmShape<BN>;
+  using S = GemmShape<CG, BN>;
   extern __shared__ unsigned char dyn[];
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], done[2], taken[2],
       drained;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort;
+  __shared__ float swap[4][32 * 33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : blockIdx.x & 1;
   const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -284,50 +376,56 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&done[a]), 1);
-      mbar_init(smem_u32(&taken[a]), 4);
+      mbar_init(smem_u32(&taken[a]), 4 * CG);
     }
     mbar_init(smem_u32(&drained), 1);
     abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&tmem_slot)),
-                 "r"(2 * BN)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(&tmem_slot), 2 * BN);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if constexpr (CG == 1)
+    __syncthreads();
+  else
+    cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_slot;
   pdl_enter();  // the operands are complete from here on
 
   const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   if (warp == 0) {
     if (lane == 0) {
       int64_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit q = unit_at<BN>(p, u);
+      for (int u = first; ok && u < units; u += stride) {
+        const Unit q = unit_at<CG, BN>(p, u);
+        const int xa = q.m0 + rank * kTileM, xb = q.n0 + rank * (BN / CG);
         for (int step = 0; step < q.steps; ++step, ++it) {
           const int s = (int)(it % S::kStages);
           const uint32_t round = (uint32_t)(it / S::kStages);
           if (!(ok = gemm_wait(smem_u32(&empty[s]), (round & 1) ^ 1, p.wait_limit, &abort))) break;
-          const uint32_t bar = smem_u32(&full[s]);
+          uint32_t bar = smem_u32(&full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(bar, CG * S::kStageBytes);
+          if constexpr (CG == 2) bar = in_cta(bar, 0);
           const uint32_t at = ring + s * S::kStageBytes;
           const int y = (int)(q.t0 + (int64_t)step * kStep);
-          mbar_arrive_expect_tx(bar, S::kStageBytes);
 #pragma unroll
-          for (int b = 0; b < kTileM / 64; ++b)
-            tma_box(at + b * kBoxBytes, &map_a, q.m0 + b * 64, y, bar);
+          for (int b = 0; b < S::kBoxesA; ++b)
+            tma_box<CG>(at + b * kBoxBytes, &map_a, xa + b * 64, y, bar);
 #pragma unroll
-          for (int b = 0; b < BN / 64; ++b)
-            tma_box(at + (kTileM / 64 + b) * kBoxBytes, &map_b, q.n0 + b * 64, y, bar);
+          for (int b = 0; b < S::kBoxesB; ++b)
+            tma_box<CG>(at + (S::kBoxesA + b) * kBoxBytes, &map_b, xb + b * 64, y, bar);
         }
       }
-      // every copy issued lands before this CTA's shared memory goes away
-      for (int s = 0; !ok && s < S::kStages; ++s) {
+      // every copy issued lands before shared memory goes away (the pair's second
+      // CTA cannot see its bytes arrive and leaves them half a millisecond)
+      if (!ok && rank != 0) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 1000000) {
+        }
+      }
+      for (int s = 0; !ok && rank == 0 && s < S::kStages; ++s) {
         const int64_t uses = it / S::kStages + (s < it % S::kStages ? 1 : 0);
         const long long t0 = clock64();
         while (uses > 0 && !mbar_test(smem_u32(&full[s]), (uint32_t)((uses - 1) & 1)) &&
@@ -337,13 +435,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc<T, BN>();
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = instr_desc<T, CG, BN>();
       int64_t it = 0;
       int count = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++count) {
-        const Unit q = unit_at<BN>(p, u);
+      for (int u = first; ok && u < units; u += stride, ++count) {
+        const Unit q = unit_at<CG, BN>(p, u);
         const int a = count & 1;
         if (!(ok = gemm_wait(smem_u32(&taken[a]), ((count >> 1) & 1) ^ 1, p.wait_limit, &abort)))
           break;
@@ -356,17 +454,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t at = ring + s * S::kStageBytes;
           const uint64_t da = operand_desc(at);
-          const uint64_t db = operand_desc(at + kTileM / 64 * kBoxBytes);
+          const uint64_t db = operand_desc(at + S::kBoxesA * kBoxBytes);
 #pragma unroll
           for (int j = 0; j < kStep / 16; ++j)  // 16 tokens are 2048 bytes further on
-            mma_16(d, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc, step > 0 || j > 0);
-          mma_commit(smem_u32(&empty[s]));
+            mma_16<CG>(d, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc, step > 0 || j > 0);
+          mma_commit<CG>(smem_u32(&empty[s]));
         }
-        if (ok) mma_commit(smem_u32(&done[a]));
+        if (ok) mma_commit<CG>(smem_u32(&done[a]));
       }
       if (!ok) {
         // products in flight end before tensor memory is given back
-        mma_commit(smem_u32(&drained));
+        mma_commit<CG>(smem_u32(&drained));
         const long long t0 = clock64();
         while (!mbar_test(smem_u32(&drained), 0) && clock64() - t0 < p.wait_limit) {
         }
@@ -376,43 +474,67 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else {
     const int quarter = warp & 3;  // the tensor-memory lanes this warp may read
     int count = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++count) {
-      const Unit q = unit_at<BN>(p, u);
+    for (int u = first; u < units; u += stride, ++count) {
+      const Unit q = unit_at<CG, BN>(p, u);
       const int a = count & 1;
       const bool ok = gemm_wait(smem_u32(&done[a]), (count >> 1) & 1, p.wait_limit, &abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int row = q.m0 + quarter * 32 + lane;
+      const int row0 = q.m0 + rank * kTileM + quarter * 32;
       for (int c = 0; c < BN && q.n0 + c < p.k; c += 32) {
         uint32_t r[32];
         tmem_load32(tmem + ((uint32_t)quarter << 21) + a * BN + c, r);
-        store32<BN>(p, q, row, q.n0 + c, r);
+        store32(p, q, row0, q.n0 + c, r, swap[quarter]);
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&taken[a]));
+      if (lane == 0) {
+        if constexpr (CG == 1)
+          mbar_arrive(smem_u32(&taken[a]));
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           in_cta(smem_u32(&taken[a]), 0))
+                       : "memory");
+      }
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if constexpr (CG == 1)
+    __syncthreads();
+  else
+    cluster_sync();  // neither CTA leaves while the other may still reach into it
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
+  if (warp == 1) tmem_free<CG>(tmem, 2 * BN);
 }
 
 // dw = the splits' partial sums in order (+ addend); without splits (no tokens)
-// the addend, or zeros.
-__global__ void __launch_bounds__(256)
+// the addend, or zeros.  Four columns a thread.
+constexpr int kSumThreads = 128;
+
+__global__ void __launch_bounds__(kSumThreads)
     act8_wgrad_sum_kernel(const __grid_constant__ GemmParams p) {
   pdl_enter();
-  const int64_t total = (int64_t)p.n * p.k;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
-       e += (int64_t)gridDim.x * 256) {
-    const int64_t i = e / p.k, j = e - i * p.k;
-    float s = 0.f;
-    for (int q = 0; q < p.splits; ++q) s += p.partial[((int64_t)q * p.n + i) * p.pk + j];
-    if (p.addend.data) s += ld_any(p.addend.data, p.out_dtype, i * p.addend.ld + j);
-    st_any(p.dw.data, p.out_dtype, i * p.dw.ld + j, s);
+  const int j = (blockIdx.x * kSumThreads + threadIdx.x) * 4;
+  if (j >= p.k) return;
+  for (int64_t i = blockIdx.y; i < p.n; i += gridDim.y) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* at = p.partial + i * p.pk + j;
+#pragma unroll 4
+    for (int q = 0; q < p.splits; ++q) {
+      const float4 x = *reinterpret_cast<const float4*>(at + (int64_t)q * p.n * p.pk);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (j + c < p.k) {
+        float x = f[c];
+        if (p.addend.data) x += ld_any(p.addend.data, p.out_dtype, i * p.addend.ld + j + c);
+        st_any(p.dw.data, p.out_dtype, i * p.dw.ld + j + c, x);
+      }
   }
 }
 
@@ -420,32 +542,53 @@ __global__ void __launch_bounds__(256)
 // host
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kSms = 152, kMinSplit = 256;
+constexpr int64_t kSms = 152;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Tile width, and how the tokens are split when there are too few tiles for the
-// SMs: functions of the sizes alone.
+// The form of a product and how its tokens are split: functions of the sizes alone.
 struct Plan {
-  int bn;
+  bool pair;  // tiles of 256 x 256 on two CTAs, or of 128 x 128 on one
   int64_t tiles_m, tiles_n, splits, per_split;
   int64_t ld_x, ld_dy, pk;
   int64_t x_bytes, dy_bytes, partial_bytes;
 };
 
+// Both forms copy 32 KB a step into each SM, which takes 512 cycles at the 64 bytes
+// a cycle that an SM gets from L2: about 0.29 us, measured alike for both.  The pair does
+// four times the products per step on two SMs (16384 x 8192 x 8192: 1.29 ms
+// against 2.30 ms), the single CTA reaches more SMs when there are few tiles
+// (257 x 768 x 768: 7.3 against 9.8 us).  So the form and the number of splits are
+// those of the least estimated time: whole waves of tiles, a step's time each,
+// the filling of the ring, and for splits a second kernel that moves the partial
+// sums at about 4 TB/s.
 Plan make_plan(int64_t tokens, int64_t n, int64_t k) {
+  constexpr double kStepUs = 0.29, kTileUs = 1.0, kLaunchUs = 3.0, kBytesPerUs = 4e6;
   Plan r{};
-  r.tiles_m = (n + kTileM - 1) / kTileM;
-  r.bn = r.tiles_m * ((k + 255) / 256) >= kSms ? 256 : 128;
-  r.tiles_n = (k + r.bn - 1) / r.bn;
-  const int64_t tiles = std::max<int64_t>(1, r.tiles_m * r.tiles_n);
-  const int64_t want = std::min(std::max<int64_t>(1, kSms / tiles),
-                                std::max<int64_t>(1, (tokens + kMinSplit - 1) / kMinSplit));
-  r.per_split = std::max<int64_t>(kStep, up((tokens + want - 1) / want, kStep));
-  r.splits = (tokens + r.per_split - 1) / r.per_split;
+  r.pk = up(k, 4);
+  double best = 0;
+  for (int pair = 1; pair >= 0; --pair) {
+    const int64_t tile = pair ? 256 : 128, slots = pair ? kSms / 2 : kSms;
+    const int64_t tm = (n + tile - 1) / tile, tn = (k + tile - 1) / tile;
+    for (int64_t want = 1; want <= 32; ++want) {
+      const int64_t per = std::max<int64_t>(kStep, up((tokens + want - 1) / want, kStep));
+      const int64_t splits = (tokens + per - 1) / per;
+      if (want > 1 && (splits != want || per < 2 * kStep)) continue;
+      const int64_t waves = (tm * tn * splits + slots - 1) / slots;
+      double us = (double)waves * ((double)(per / kStep) * kStepUs + kTileUs);
+      if (splits > 1)
+        us += kLaunchUs + (double)(splits + 1) * (double)n * (double)r.pk * 4 / kBytesPerUs;
+      if (best > 0 && us >= best) continue;
+      best = us;
+      r.pair = pair;
+      r.tiles_m = tm;
+      r.tiles_n = tn;
+      r.splits = splits;
+      r.per_split = per;
+    }
+  }
   r.ld_x = up(k, 64);
   r.ld_dy = up(n, 64);
-  r.pk = up(k, 4);
   r.x_bytes = up(tokens * r.ld_x * 2, 256);
   r.dy_bytes = up(tokens * r.ld_dy * 2, 256);
   r.partial_bytes = r.splits > 1 ? r.splits * n * r.pk * 4 : 0;
@@ -483,20 +626,31 @@ int encode(CUtensorMap* map, bool is_bf16, const void* base, int64_t cols, int64
   return DPOPT_OK;
 }
 
-template <class T, int BN>
+template <class T, int CG, int BN>
 int launch_gemm(const GemmParams& p, const CUtensorMap& a, const CUtensorMap& b,
                 cudaStream_t stream) {
-  auto kern = act8_wgrad_kernel<T, BN>;
-  const size_t smem = GemmShape<BN>::kSmem;
+  auto kern = act8_wgrad_kernel<T, CG, BN>;
+  const size_t smem = GemmShape<CG, BN>::kSmem;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "shared memory size");
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-  const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
-  return launched(launch_pdl(kern, grid, kGemmThreads, smem, stream, p, a, b),
-                  "act8 weight gradient");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, sms / CG) * CG));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return launched(cudaLaunchKernelEx(&cfg, kern, p, a, b), "act8 weight gradient");
 }
 
 template <class T>
@@ -522,9 +676,8 @@ int run_wgrad(const Plan& plan, GemmParams& g, OperandParams& o, unsigned char* 
   DPOPT_TRY(launched(
       launch_pdl(act8_operands_kernel<T>, ctas, kOperandThreads, 0, stream, o),
       "act8 weight gradient operands"));
-  DPOPT_TRY(plan.bn == 256 ? launch_gemm<T, 256>(g, a, b, stream)
-                           : launch_gemm<T, 128>(g, a, b, stream));
-  return DPOPT_OK;
+  return plan.pair ? launch_gemm<T, 2, 256>(g, a, b, stream)
+                   : launch_gemm<T, 1, 128>(g, a, b, stream);
 }
 
 }  // namespace
@@ -623,10 +776,9 @@ int dpopt_act8_wgrad(const void* dy, int dtype, int64_t ld_dy, const int8_t* cod
                                        : run_wgrad<fp16>(plan, g, o, at, st));
     if (plan.splits == 1) return DPOPT_OK;
   }
-  int sms = 0;
-  DPOPT_TRY(sm_count(&sms));
-  const unsigned ctas = (unsigned)std::min<int64_t>((n * k + 255) / 256, (int64_t)sms * 8);
-  return launched(launch_pdl(act8_wgrad_sum_kernel, ctas, 256, 0, st, g),
+  const dim3 ctas((unsigned)((k + 4 * kSumThreads - 1) / (4 * kSumThreads)),
+                  (unsigned)std::min<int64_t>(n, 65535));
+  return launched(launch_pdl(act8_wgrad_sum_kernel, ctas, dim3(kSumThreads), 0, st, g),
                   "act8 weight gradient sum");
 }
 
