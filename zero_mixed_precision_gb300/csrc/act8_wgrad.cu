@@ -559,11 +559,11 @@ struct Plan {
 // four times the products per step on two SMs (16384 x 8192 x 8192: 1.29 ms
 // against 2.30 ms), the single CTA reaches more SMs when there are few tiles
 // (257 x 768 x 768: 7.3 against 9.8 us).  So the form and the number of splits are
-// those of the least estimated time: whole waves of tiles, a step's time each,
-// the filling of the ring, and for splits a second kernel that moves the partial
-// sums at about 4 TB/s.
+// those of the least estimated time: whole waves of tiles, a step's time each, a
+// tile's way out (3 and 1.5 us), and for splits a second kernel that moves the
+// partial sums at about 4 TB/s.
 Plan make_plan(int64_t tokens, int64_t n, int64_t k) {
-  constexpr double kStepUs = 0.29, kTileUs = 1.0, kLaunchUs = 3.0, kBytesPerUs = 4e6;
+  constexpr double kStepUs = 0.29, kLaunchUs = 3.0, kBytesPerUs = 4e6;
   Plan r{};
   r.pk = up(k, 4);
   double best = 0;
@@ -575,7 +575,7 @@ Plan make_plan(int64_t tokens, int64_t n, int64_t k) {
       const int64_t splits = (tokens + per - 1) / per;
       if (want > 1 && (splits != want || per < 2 * kStep)) continue;
       const int64_t waves = (tm * tn * splits + slots - 1) / slots;
-      double us = (double)waves * ((double)(per / kStep) * kStepUs + kTileUs);
+      double us = (double)waves * ((double)(per / kStep) * kStepUs + (pair ? 3.0 : 1.5));
       if (splits > 1)
         us += kLaunchUs + (double)(splits + 1) * (double)n * (double)r.pk * 4 / kBytesPerUs;
       if (best > 0 && us >= best) continue;

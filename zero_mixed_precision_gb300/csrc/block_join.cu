@@ -8,15 +8,15 @@
 namespace dpopt {
 namespace {
 
-// A row is held by one CTA of tpr threads (a multiple of 32), in NV fragments of 8
-// columns per thread: as few as 512 threads can cover the row with.  In the
-// vector form (VEC: every matrix may be moved 16 bytes at a time) thread t's
-// fragment v is the columns (v tpr + t) 8 .. + 7; in the element form, for odd
-// widths and alignments, its element i is column (v 8 + i) tpr + t, so that a
-// warp always touches neighbouring columns.  Either way a block of 32 columns
-// lies in one warp.  The row index depends on blockIdx alone, which keeps the
-// row addresses out of the threads' registers.
-constexpr int kJoinCta = 512, kJoinSms = 152;
+// A row is held by one CTA of tpr threads (a multiple of 32), 16 columns a thread
+// (32 beyond 8192 columns) as fragments of 8.  In the vector form (every matrix
+// may be moved 16 bytes at a time, up to 8192 columns) thread t's fragment v is the
+// columns (v tpr + t) 8 .. + 7; in the element form its element i is column
+// (v 8 + i) tpr + t, so that a warp always touches neighbouring columns.  Either
+// way a block of 32 columns lies in one warp.  The row index depends on blockIdx
+// alone, which keeps row addresses out of the threads' registers.
+constexpr int kJoinCta = 512, kJoinSms = 152, kVecFrags = 2;
+constexpr int kVecCols = kJoinCta * 8 * kVecFrags;
 
 struct JoinParams {
   int64_t rows;
@@ -30,7 +30,7 @@ struct JoinParams {
   Dbg dbg;
 };
 
-__host__ __device__ inline int row_frags(int64_t cols) { return cols <= 8 * kJoinCta ? 1 : cols <= 16 * kJoinCta ? 2 : 4; }
+__host__ __device__ inline int row_frags(int64_t cols) { return cols <= kVecCols ? 2 : 4; }
 __host__ __device__ inline int row_threads(int64_t cols) {
   const int64_t per_warp = 256 * row_frags(cols);
   return (int)((cols + per_warp - 1) / per_warp) * 32;
@@ -79,7 +79,7 @@ __device__ __noinline__ void stage_param(const void* w, int dtype, int64_t at, i
     }
 }
 
-__device__ __forceinline__ int64_t gate_row_of(int64_t gate_rows, int64_t row) {
+__host__ __device__ inline int64_t gate_row_of(int64_t gate_rows, int64_t row) {
   return gate_rows > 0 ? row / gate_rows : 0;
 }
 
@@ -87,7 +87,7 @@ __device__ __forceinline__ int64_t gate_row_of(int64_t gate_rows, int64_t row) {
 // two sums, and h_out stays in registers in fp32 between the norms.  The
 // parameters are kept as branch_scale * gate * w_post and w_pre.
 template <class T, bool VEC, int NV>
-__global__ void __launch_bounds__(kJoinCta, NV == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kJoinCta, 1)
     block_join_kernel(const __grid_constant__ JoinParams p) {
   pdl_enter();
   __shared__ float slot[2][kJoinCta / 32][1];
@@ -222,13 +222,12 @@ enum { kPartWPre = 0, kPartWPost = 1, kPartGateFirst = 2, kPartGateLast = 3, kPa
 struct JoinGradParams {
   int64_t rows, per, parts;  // rows of a part, parts
   int cols, width, tpr;      // width: cols rounded up to whole blocks
-  // the vector form's ring in shared memory: rows held, bytes of one, and where and
-  // how large the fragments of each array are (enum kIn*)
-  int stages;
-  uint32_t stage_bytes, frag_at[4], frag_bytes[4];
+  int stages;                // the vector form's ring: rows held,
+  uint32_t stage_bytes;      // bytes of one
   int param_dtype;
   float res_scale, branch_scale;
   int64_t gate_rows;
+  int by_gate;  // the finish kernel's sums of dgate: by gate row, or by part
   Mat dh_out, du, y, h_out, gate, dh, dy, dgate;
   Act8Out y8, h8;
   const void *w_post, *w_pre;
@@ -256,129 +255,262 @@ __device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The four arrays a gradient row reads, as a thread gets at its fragments.
-// Vector form: a ring of rows in shared memory, each thread copying (cp.async) and
-// reading only its own fragments, so that rows are in flight without registers
-// and without barriers.  Element form: straight from global memory (the second
-// reading of a row comes from L1).
-enum { kInDh = 0, kInDu = 1, kInY = 2, kInH = 3 };
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
 
-template <class T, bool VEC, int NV>
-struct GradRow {
+// The rows of a run as a thread gets at its fragments of the four arrays (kDh ..
+// kH); begin() and end() stand around each row.
+enum { kDh = 0, kDu = 1, kY = 2, kH = 3 };
+
+// Vector form.  Rows come through a ring in shared memory: each thread copies
+// (cp.async) and reads only its own fragments, so that up to three rows are in
+// flight without registers and without barriers.  YP: y comes packed; HP: h_out
+// absent (0), as a matrix (1), packed (2).  Places of columns past the row hold
+// zeros throughout.
+template <class T, int YP, int HP>
+struct VecRows {
+  static constexpr int NV = kVecFrags;
+  static constexpr uint32_t kWide = 8 * sizeof(T), kNarrow = 8;
+  static constexpr uint32_t kYBytes = YP ? kNarrow : kWide, kHBytes = HP == 2 ? kNarrow : kWide;
+  const JoinGradParams& p;
+  const int tpr;
+  int c[NV];
+  bool on[NV];
+  uint32_t at[4];  // this thread's first fragment of each array in stage 0
+  int stage = 0;
+  // rows still to be asked for, and the addresses of the next one
+  int64_t left;
+  const T *dh_in, *du_in, *y_in, *h_in;
+  const int8_t *y_codes, *h_codes;
+  const uint8_t *y_exps, *h_exps;  // of the row after the present one
+  const float *r_pre, *r_post;
+  T *dh_out, *dy_out;
+  uint32_t y_byte[NV], h_byte[NV];
+  float y_scale[NV], h_scale[NV];
+  float next_r1 = 0.f, next_r2 = 1.f, r1 = 0.f, r2 = 1.f;
+  int64_t ahead;  // rows whose small values are still to be asked for
+
+  // bytes of a stage for tpr threads
+  static constexpr uint32_t stage_bytes(int tpr) {
+    return NV * tpr * (kWide + (HP ? kWide : 0) + kYBytes + (HP ? kHBytes : 0));
+  }
+  __device__ __forceinline__ VecRows(const JoinGradParams& q, int64_t lo, int64_t hi,
+                                     uint32_t ring)
+      : p(q), tpr(blockDim.x), left(hi - lo), ahead(hi - lo) {
+    const int t = threadIdx.x;
+    const uint32_t wide = NV * tpr * kWide;
+    at[kDh] = ring + t * kWide;
+    at[kDu] = at[kDh] + wide;
+    at[kY] = ring + (HP ? 2 : 1) * wide + t * kYBytes;
+    at[kH] = ring + (HP ? 2 : 1) * wide + NV * tpr * kYBytes + t * kHBytes;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      c[v] = (v * tpr + t) * 8;
+      on[v] = c[v] < p.cols;
+      y_byte[v] = h_byte[v] = 0;
+    }
+    dh_in = static_cast<const T*>(p.dh_out.data) + lo * p.dh_out.ld;
+    if constexpr (YP) {
+      y_codes = p.y8.codes + lo * p.y8.ld_codes;
+      y_exps = p.y8.exps + lo * p.y8.ld_exps;
+    } else {
+      y_in = static_cast<const T*>(p.y.data) + lo * p.y.ld;
+    }
+    if constexpr (HP != 0) {
+      du_in = static_cast<const T*>(p.du.data) + lo * p.du.ld;
+      r_pre = p.rstd_pre + lo;
+    }
+    if constexpr (HP == 1) h_in = static_cast<const T*>(p.h_out.data) + lo * p.h_out.ld;
+    if constexpr (HP == 2) {
+      h_codes = p.h8.codes + lo * p.h8.ld_codes;
+      h_exps = p.h8.exps + lo * p.h8.ld_exps;
+    }
+    r_post = p.rstd_post ? p.rstd_post + lo : nullptr;
+    dh_out = p.dh.data ? static_cast<T*>(p.dh.data) + lo * p.dh.ld : nullptr;
+    dy_out = static_cast<T*>(p.dy.data) + lo * p.dy.ld;
+    for (int s = 0; s < p.stages; ++s)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (!on[v]) {
+          clear(at[kDh] + s * p.stage_bytes + v * tpr * kWide, kWide);
+          if (HP) clear(at[kDu] + s * p.stage_bytes + v * tpr * kWide, kWide);
+          clear(at[kY] + s * p.stage_bytes + v * tpr * kYBytes, kYBytes);
+          if (HP) clear(at[kH] + s * p.stage_bytes + v * tpr * kHBytes, kHBytes);
+        }
+    for (int s = 0; s < p.stages; ++s) fetch(s);
+    small();
+  }
+  __device__ __forceinline__ void clear(uint32_t a, uint32_t bytes) {
+    for (uint32_t i = 0; i < bytes; i += 8)
+      asm volatile("st.shared.v2.u32 [%0], {%1,%1};" ::"r"(a + i), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ void wide_in(uint32_t a, const T* src) {
+    copy_async16(a, src);
+    if constexpr (sizeof(T) == 4) copy_async16(a + 16, src + 4);
+  }
+  // Start the copies of the next row into a stage.
+  __device__ __forceinline__ void fetch(int s) {
+    if (left > 0) {
+      --left;
+      const uint32_t so = s * p.stage_bytes;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (on[v]) {
+          wide_in(at[kDh] + so + v * tpr * kWide, dh_in + c[v]);
+          if constexpr (HP != 0) wide_in(at[kDu] + so + v * tpr * kWide, du_in + c[v]);
+          if constexpr (YP)
+            copy_async8(at[kY] + so + v * tpr * kYBytes, y_codes + c[v]);
+          else
+            wide_in(at[kY] + so + v * tpr * kYBytes, y_in + c[v]);
+          if constexpr (HP == 1) wide_in(at[kH] + so + v * tpr * kHBytes, h_in + c[v]);
+          if constexpr (HP == 2) copy_async8(at[kH] + so + v * tpr * kHBytes, h_codes + c[v]);
+        }
+      dh_in += p.dh_out.ld;
+      if constexpr (YP)
+        y_codes += p.y8.ld_codes;
+      else
+        y_in += p.y.ld;
+      if constexpr (HP != 0) du_in += p.du.ld;
+      if constexpr (HP == 1) h_in += p.h_out.ld;
+      if constexpr (HP == 2) h_codes += p.h8.ld_codes;
+    }
+    copy_commit();
+  }
+  // Exponent bytes and statistics of the next row, asked for one row ahead.
+  __device__ __forceinline__ void small() {
+    if (ahead-- <= 0) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (YP && on[v]) y_byte[v] = y_exps[c[v] / kAct8Block];
+      if (HP == 2 && on[v]) h_byte[v] = h_exps[c[v] / kAct8Block];
+    }
+    if constexpr (YP) y_exps += p.y8.ld_exps;
+    if constexpr (HP == 2) h_exps += p.h8.ld_exps;
+    if constexpr (HP != 0) next_r1 = *r_pre++;
+    if (r_post) next_r2 = *r_post++;
+  }
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if constexpr (YP) y_scale[v] = act8_scale(y_byte[v]);
+      if constexpr (HP == 2) h_scale[v] = act8_scale(h_byte[v]);
+    }
+    r1 = next_r1;
+    r2 = next_r2;
+    small();
+    // the oldest of the rows asked for has arrived
+    if (p.stages == 1)
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (p.stages == 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+  }
+  template <int WHICH>
+  __device__ __forceinline__ void get(int v, float (&f)[8]) const {
+    constexpr bool none = HP == 0 && (WHICH == kDu || WHICH == kH);
+    constexpr bool narrow = (WHICH == kY && YP) || (WHICH == kH && HP == 2);
+    if constexpr (none) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    } else if constexpr (narrow) {
+      uint2 k;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(k.x), "=r"(k.y)
+                   : "r"(at[WHICH] + stage * p.stage_bytes + v * tpr * kNarrow)
+                   : "memory");
+      act8_values(k, WHICH == kY ? y_scale[v] : h_scale[v], f);
+    } else {
+      const uint32_t a = at[WHICH] + stage * p.stage_bytes + v * tpr * kWide;
+      Raw8<T> r;
+      r.v = ld_shared16(a);
+      if constexpr (sizeof(T) == 4) r.w = ld_shared16(a + 16);
+      widen8<T>(r, f);
+    }
+  }
+  __device__ __forceinline__ bool wants_dh() const { return dh_out != nullptr; }
+  __device__ __forceinline__ void put_dh(int v, const float (&f)[8]) const {
+    if (on[v]) st_vec8<T>(dh_out + c[v], f);
+  }
+  __device__ __forceinline__ void put_dy(int v, const float (&f)[8]) const {
+    if (on[v]) st_vec8<T>(dy_out + c[v], f);
+  }
+  __device__ __forceinline__ void end() {
+    if (dh_out) dh_out += p.dh.ld;
+    dy_out += p.dy.ld;
+    fetch(stage);
+    stage = stage + 1 == p.stages ? 0 : stage + 1;
+  }
+};
+
+// Element form: straight from global memory, the second reading of a row from L1.
+template <class T, int NV_>
+struct ElemRows {
+  static constexpr int NV = NV_;
   const JoinGradParams& p;
   const int t, tpr;
-  // this thread's places in a stage of the ring: 16 or 32 bytes a fragment, and 8
-  const uint32_t ring;
-  uint32_t next[2][NV];  // exponent bytes of y and h of the row after the present one
-  float scale[2][NV];    // and the present row's scales
+  int64_t row;
+  float r1 = 0.f, r2 = 1.f;
 
-  __device__ __forceinline__ GradRow(const JoinGradParams& q, uint32_t r)
-      : p(q), t(threadIdx.x), tpr(blockDim.x), ring(r) {}
-
-  __device__ __forceinline__ const Mat& mat(int which) const {
-    return which == kInDh ? p.dh_out : which == kInDu ? p.du : which == kInY ? p.y : p.h_out;
+  __device__ __forceinline__ ElemRows(const JoinGradParams& q, int64_t lo, int64_t, uint32_t)
+      : p(q), t(threadIdx.x), tpr(blockDim.x), row(lo) {}
+  __device__ __forceinline__ void begin() {
+    if (p.du.data) r1 = p.rstd_pre[row];
+    if (p.rstd_post) r2 = p.rstd_post[row];
   }
-  __device__ __forceinline__ const Act8Out& act(int which) const {
-    return which == kInY ? p.y8 : p.h8;
-  }
-  __device__ __forceinline__ bool packed(int which) const {
-    return which == kInY ? p.y8.codes != nullptr : which == kInH && p.h8.codes != nullptr;
-  }
-  __device__ __forceinline__ bool present(int which) const {
-    return which == kInDh || which == kInY || p.du.data != nullptr;
-  }
-  __device__ __forceinline__ uint32_t slot(uint32_t at, int which, int v) const {
-    return at + p.frag_at[which] + (v * tpr + t) * p.frag_bytes[which];
-  }
-
-  // Start the copies of a row into the stage at `at`.
-  __device__ __forceinline__ void fetch(int64_t row, uint32_t at) const {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void from_matrix(const Mat& m, int v, float (&f)[8]) const {
+    const T* q = static_cast<const T*>(m.data) + row * m.ld;
 #pragma unroll
-      for (int which = 0; which < 4; ++which) {
-        if (!present(which)) continue;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = column<true>(v, 0, t, tpr);
-          if (c >= p.cols) continue;
-          if (packed(which)) {
-            copy_async8(slot(at, which, v), act(which).codes + row * act(which).ld_codes + c);
-          } else {
-            const T* src = static_cast<const T*>(mat(which).data) + row * mat(which).ld + c;
-            copy_async16(slot(at, which, v), src);
-            if constexpr (sizeof(T) == 4) copy_async16(slot(at, which, v) + 16, src + 4);
-          }
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<false>(v, i, t, tpr);
+      if (c < p.cols) f[i] = to_f32(q[c]);
     }
   }
-  // The exponent bytes of a row, asked for one row ahead.
-  __device__ __forceinline__ void fetch_scales(int64_t row) {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void from_packed(const Act8Out& o, int v, float (&f)[8]) const {
+    const int8_t* codes = o.codes + row * o.ld_codes;
+    const uint8_t* exps = o.exps + row * o.ld_exps;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (packed(kInY + k) && present(kInY + k)) {
-          const uint8_t* exps = act(kInY + k).exps + row * act(kInY + k).ld_exps;
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int c = column<true>(v, 0, t, tpr);
-            next[k][v] = c < p.cols ? exps[c / kAct8Block] : 0;
-          }
-        }
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<false>(v, i, t, tpr);
+      if (c < p.cols) f[i] = (float)codes[c] * act8_scale(exps[c / kAct8Block]);
     }
   }
-  __device__ __forceinline__ void take_scales() {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (packed(kInY + k) && present(kInY + k))
-#pragma unroll
-          for (int v = 0; v < NV; ++v) scale[k][v] = act8_scale(next[k][v]);
-    }
-  }
-
-  __device__ __forceinline__ void get(int64_t row, uint32_t at, int which, int v,
-                                      float (&f)[8]) const {
+  template <int WHICH>
+  __device__ __forceinline__ void get(int v, float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    if (!present(which)) return;
-    if constexpr (VEC) {
-      if (column<true>(v, 0, t, tpr) >= p.cols) return;
-      const uint32_t a = slot(at, which, v);
-      if (packed(which)) {
-        uint2 c;
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(a) : "memory");
-        act8_values(c, scale[which - kInY][v], f);
-        return;
-      }
-      Raw8<T> r;
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
-                   : "r"(a)
-                   : "memory");
-      if constexpr (sizeof(T) == 4)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r.w.x), "=r"(r.w.y), "=r"(r.w.z), "=r"(r.w.w)
-                     : "r"(a + 16)
-                     : "memory");
-      widen8<T>(r, f);
-    } else if (packed(which)) {
-      const int8_t* codes = act(which).codes + row * act(which).ld_codes;
-      const uint8_t* exps = act(which).exps + row * act(which).ld_exps;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = column<false>(v, i, t, tpr);
-        if (c < p.cols) f[i] = (float)codes[c] * act8_scale(exps[c / kAct8Block]);
-      }
-    } else {
-      const T* q = static_cast<const T*>(mat(which).data) + row * mat(which).ld;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = column<false>(v, i, t, tpr);
-        if (c < p.cols) f[i] = to_f32(q[c]);
-      }
+    if (WHICH == kDh) from_matrix(p.dh_out, v, f);
+    if (WHICH == kDu && p.du.data) from_matrix(p.du, v, f);
+    if (WHICH == kY) {
+      if (p.y8.codes)
+        from_packed(p.y8, v, f);
+      else
+        from_matrix(p.y, v, f);
+    }
+    if (WHICH == kH && p.du.data) {
+      if (p.h8.codes)
+        from_packed(p.h8, v, f);
+      else
+        from_matrix(p.h_out, v, f);
     }
   }
+  __device__ __forceinline__ bool wants_dh() const { return p.dh.data != nullptr; }
+  __device__ __forceinline__ void put_dh(int v, const float (&f)[8]) const {
+    frag_store<T, false>(p.dh, row, v, t, tpr, p.cols, f);
+  }
+  __device__ __forceinline__ void put_dy(int v, const float (&f)[8]) const {
+    frag_store<T, false>(p.dy, row, v, t, tpr, p.cols, f);
+  }
+  __device__ __forceinline__ void end() { ++row; }
 };
 
 // At the end of a gate row's rows in a part: its sums branch_scale * e (in `mine`)
@@ -417,10 +549,11 @@ __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t par
 // Sums over rows per column: dw_pre, and e = sum d y rstd_post, from which, while
 // the gate row stays the same, dw_post grows by branch gate e and dgate is branch
 // w_post e.
-template <class T, bool VEC, int NV>
+template <class T, bool VEC, class Rows>
 __global__ void __launch_bounds__(kJoinCta, 1)
     block_join_grad_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
+  constexpr int NV = Rows::NV;
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float slot[2][kJoinCta / 32][3];
   const int t = threadIdx.x, tpr = blockDim.x;
@@ -431,8 +564,7 @@ __global__ void __launch_bounds__(kJoinCta, 1)
   // place per column of a thread
   float* post = reinterpret_cast<float*>(dyn) + t;
   float* mine = post + 8 * NV * tpr;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dyn) + 16 * NV * tpr * 4;
-  GradRow<T, VEC, NV> in(p, ring);
+  Rows in(p, lo, hi, (uint32_t)__cvta_generic_to_shared(dyn) + 16 * NV * tpr * 4);
   float wpre[NV][8], q[NV][8], acc[NV][8], e[NV][8];
   stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
 #pragma unroll
@@ -443,18 +575,12 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       acc[v][i] = e[v][i] = 0.f;
       post[(v * 8 + i) * tpr] = 0.f;
     }
-  for (int s = 0; s < p.stages; ++s) {
-    if (lo + s < hi) in.fetch(lo + s, ring + s * p.stage_bytes);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  in.fetch_scales(lo);
-  int64_t held = -1;
-  bool first_gate = true;
-  int stage = 0;
+  int64_t grow = gate_row_of(p.gate_rows, lo);
+  int64_t gate_end = p.gate_rows > 0 ? min(hi, (grow + 1) * p.gate_rows) : hi;
+  bool first_gate = true, new_gate = true;
   for (int64_t row = lo; row < hi; ++row) {
-    const int64_t grow = gate_row_of(p.gate_rows, row);
-    if (grow != held) {
-      held = grow;
+    if (new_gate) {
+      new_gate = false;
       stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -469,20 +595,8 @@ __global__ void __launch_bounds__(kJoinCta, 1)
           for (int i = 0; i < 8; ++i) q[v][i] *= mine[(v * 8 + i) * tpr];
       }
     }
-    const float r1 = p.du.data ? p.rstd_pre[row] : 0.f;
-    const float r2 = p.rstd_post ? p.rstd_post[row] : 1.f;
-    in.take_scales();
-    if (row + 1 < hi) in.fetch_scales(row + 1);
-    const uint32_t at = ring + stage * p.stage_bytes;
-    if constexpr (VEC) {
-      // the oldest of the rows asked for has arrived
-      if (p.stages == 1)
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else if (p.stages == 2)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    }
+    in.begin();
+    const float r1 = in.r1, r2 = in.r2;
     float sum[3];
     {
       uint64_t s2 = 0, a2 = 0, b2 = 0;
@@ -490,10 +604,10 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float d[8], u[8], h[8], y[8];
-        in.get(row, at, kInDh, v, d);
-        in.get(row, at, kInDu, v, u);
-        in.get(row, at, kInY, v, y);
-        in.get(row, at, kInH, v, h);
+        in.template get<kDh>(v, d);
+        in.template get<kDu>(v, u);
+        in.template get<kY>(v, y);
+        in.template get<kH>(v, h);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint64_t wu = mul2(pair(wpre[v][i], wpre[v][i + 1]), pair(u[i], u[i + 1]));
@@ -517,10 +631,10 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float d[8], u[8], h[8], y[8];
-        in.get(row, at, kInDh, v, d);
-        in.get(row, at, kInDu, v, u);
-        in.get(row, at, kInY, v, y);
-        in.get(row, at, kInH, v, h);
+        in.template get<kDh>(v, d);
+        in.template get<kDu>(v, u);
+        in.template get<kY>(v, y);
+        in.template get<kH>(v, h);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint64_t u2 = pair(u[i], u[i + 1]), y2 = pair(y[i], y[i + 1]);
@@ -541,23 +655,18 @@ __global__ void __launch_bounds__(kJoinCta, 1)
           u[i] = lane0(dy);
           u[i + 1] = lane1(dy);
         }
-        if (p.dh.data) {
+        if (in.wants_dh()) {
           if (p.res_scale != 1.f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] *= p.res_scale;
           }
-          frag_store<T, VEC>(p.dh, row, v, t, tpr, p.cols, d);
+          in.put_dh(v, d);
         }
-        frag_store<T, VEC>(p.dy, row, v, t, tpr, p.cols, u);
+        in.put_dy(v, u);
       }
     }
-    if constexpr (VEC) {
-      if (row + p.stages < hi) in.fetch(row + p.stages, at);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      stage = stage + 1 == p.stages ? 0 : stage + 1;
-    }
-    if (row + 1 == hi || gate_row_of(p.gate_rows, row + 1) != grow) {
-      // the last row here of its gate row
+    in.end();
+    if (row + 1 == gate_end) {  // the last row here of its gate row
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -567,6 +676,9 @@ __global__ void __launch_bounds__(kJoinCta, 1)
         }
       close_gate_row<VEC, NV>(p, blockIdx.x, lo, hi, row, first_gate, t, post, mine, tpr);
       first_gate = false;
+      new_gate = true;
+      ++grow;
+      gate_end = min(hi, gate_end + p.gate_rows);
     }
   }
 #pragma unroll
@@ -580,54 +692,55 @@ __global__ void __launch_bounds__(kJoinCta, 1)
     }
 }
 
-// Adds the parts' partial rows.  blockIdx.y: 0 dw_pre, 1 dw_post, 2 + q the gate
-// row that begins in part q and reaches into part q + 1 (with one gate row
-// for all rows, q = 0).  32 columns x 8 runs of parts per CTA; the runs' sums
-// are added in order.
-constexpr int kFinishRuns = 8;
+// Adds the parts' partial rows.  blockIdx.y: 0 dw_pre, 1 dw_post, from 2 on the
+// gate rows that cross a part's border: gate row blockIdx.y - 2 (when there are
+// fewer gate rows than parts), or the one that begins in part blockIdx.y - 2 and
+// reaches into the next.  32 columns x 16 runs of parts per CTA; a run adds its
+// parts in order, then the runs' sums are added in order.
+constexpr int kFinishRuns = 16;
 
 __global__ void __launch_bounds__(32 * kFinishRuns)
-block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
+    block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   __shared__ float run_sum[kFinishRuns][33];
-  const int64_t parts = p.parts, per = p.per;
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
-  int slot = blockIdx.y;
-  int64_t first = 0, last = parts;  // parts [first, last)
-  int64_t out_row = 0;
+  const int col = blockIdx.x * 32 + lane;
+  const int64_t parts = p.parts, per = p.per;
+  int64_t first = 0, last = parts, out_row = 0;  // parts [first, last)
+  int slot = blockIdx.y, first_slot = slot;
   void* out = blockIdx.y == 0 ? p.dw_pre : p.dw_post;
   if (blockIdx.y >= 2) {
     out = p.dgate.data;
-    const int64_t q = blockIdx.y - 2;
+    slot = first_slot = kPartGateFirst;
     if (p.rows > 0) {
+      const int64_t q = blockIdx.y - 2;
+      const int64_t row = p.by_gate ? q * p.gate_rows : min(p.rows, (q + 1) * per) - 1;
       int64_t glo, ghi;
-      const int64_t end = min(p.rows, (q + 1) * per);
-      gate_span(p.gate_rows, p.rows, end - 1, &glo, &ghi);
-      if (glo < q * per || (ghi <= end && !(q == 0 && parts == 0))) out = nullptr;
-      first = q;
+      gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
+      first = glo / per;
       last = (ghi + per - 1) / per;
-      out_row = gate_row_of(p.gate_rows, end - 1);
+      out_row = gate_row_of(p.gate_rows, row);
+      // inside one part: stored there; found in an earlier part: that one's
+      if (last - first == 1 || (!p.by_gate && first != q)) out = nullptr;
+      if (gate_row_of(p.gate_rows, first * per) != out_row) first_slot = kPartGateLast;
     }
   }
   if (!out) return;
   float s = 0.f;
   const int64_t each = (last - first + kFinishRuns - 1) / kFinishRuns;
-  const int64_t a = first + run * each, b = min(last, a + each);
-  if (col < p.cols) {
-    for (int64_t q = a; q < b; ++q) {
-      int use = slot;
-      if (blockIdx.y >= 2) {
-        int64_t glo, ghi;
-        gate_span(p.gate_rows, p.rows, q * per, &glo, &ghi);
-        use = gate_row_of(p.gate_rows, q * per) == out_row ? kPartGateFirst : kPartGateLast;
-      }
-      s += part_row(p, q, use)[col];
-    }
+  int64_t a = first + run * each;
+  const int64_t b = min(last, a + each);
+  if (col < p.cols && a < b) {
+    const float* at = part_row(p, a, a == first ? first_slot : slot) + col;
+    s = *at;
+    at = part_row(p, a + 1, slot) + col;
+#pragma unroll 8
+    for (++a; a < b; ++a, at += kPartSlots * p.width) s += *at;
   }
   run_sum[run][lane] = s;
   __syncthreads();
   if (run != 0 || col >= p.cols) return;
+#pragma unroll
   for (int i = 1; i < kFinishRuns; ++i) s += run_sum[i][lane];
   if (blockIdx.y < 2)
     st_any(out, p.param_dtype, col, s);
@@ -695,21 +808,15 @@ int launch_join_at(JoinParams& p, cudaStream_t stream) {
 
 template <class T>
 int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
-  switch (row_frags(p.cols)) {
-    case 1:
-      return vec ? launch_join_at<T, true, 1>(p, stream) : launch_join_at<T, false, 1>(p, stream);
-    case 2:
-      return vec ? launch_join_at<T, true, 2>(p, stream) : launch_join_at<T, false, 2>(p, stream);
-    default:
-      return vec ? launch_join_at<T, true, 4>(p, stream) : launch_join_at<T, false, 4>(p, stream);
-  }
+  if (vec) return launch_join_at<T, true, kVecFrags>(p, stream);
+  return row_frags(p.cols) == 2 ? launch_join_at<T, false, 2>(p, stream)
+                                : launch_join_at<T, false, 4>(p, stream);
 }
 
-template <class T, bool VEC, int NV>
-int launch_join_grad_at(JoinGradParams& p, cudaStream_t stream) {
-  auto kern = block_join_grad_kernel<T, VEC, NV>;
-  const size_t room = kJoinSmem / ctas_per_sm(p.cols);
-  const size_t sums = (size_t)p.tpr * 16 * NV * sizeof(float);
+template <class T, bool VEC, class Rows>
+int launch_grad_at(JoinGradParams& p, size_t room, cudaStream_t stream) {
+  auto kern = block_join_grad_kernel<T, VEC, Rows>;
+  const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
   p.stages = VEC ? (int)std::min<size_t>(3, (room - sums) / p.stage_bytes) : 0;
   const size_t smem = sums + (size_t)p.stages * p.stage_bytes;
   DPOPT_TRY(allow_smem(kern, smem));
@@ -717,30 +824,27 @@ int launch_join_grad_at(JoinGradParams& p, cudaStream_t stream) {
                   "block join gradient");
 }
 
+template <class T, int YP, int HP>
+int launch_grad_vec(JoinGradParams& p, cudaStream_t stream) {
+  using Rows = VecRows<T, YP, HP>;
+  const size_t room = kJoinSmem / ctas_per_sm(p.cols);
+  const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
+  p.stage_bytes = Rows::stage_bytes(p.tpr);
+  // the ring needs room for at least one row
+  if (sums + p.stage_bytes > room) return launch_grad_at<T, false, ElemRows<T, 2>>(p, room, stream);
+  return launch_grad_at<T, true, Rows>(p, room, stream);
+}
+
 template <class T>
 int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
-  const int nv = row_frags(p.cols);
-  p.stage_bytes = 0;
-  for (int which = 0; which < 4; ++which) {
-    const bool packed = (which == kInY && p.y8.codes) || (which == kInH && p.h8.codes);
-    p.frag_at[which] = p.stage_bytes;
-    p.frag_bytes[which] = packed ? 8 : 8 * sizeof(T);
-    if (which == kInDh || which == kInY || p.du.data)
-      p.stage_bytes += p.frag_bytes[which] * nv * p.tpr;
-  }
-  // the vector form needs room for at least one row of the ring
-  vec = vec && p.tpr * 16 * nv * sizeof(float) + p.stage_bytes <= kJoinSmem / ctas_per_sm(p.cols);
-  switch (nv) {
-    case 1:
-      return vec ? launch_join_grad_at<T, true, 1>(p, stream)
-                 : launch_join_grad_at<T, false, 1>(p, stream);
-    case 2:
-      return vec ? launch_join_grad_at<T, true, 2>(p, stream)
-                 : launch_join_grad_at<T, false, 2>(p, stream);
-    default:
-      return vec ? launch_join_grad_at<T, true, 4>(p, stream)
-                 : launch_join_grad_at<T, false, 4>(p, stream);
-  }
+  if (!vec)
+    return row_frags(p.cols) == 2 ? launch_grad_at<T, false, ElemRows<T, 2>>(p, 0, stream)
+                                  : launch_grad_at<T, false, ElemRows<T, 4>>(p, 0, stream);
+  if (!p.du.data)
+    return p.y8.codes ? launch_grad_vec<T, 1, 0>(p, stream) : launch_grad_vec<T, 0, 0>(p, stream);
+  if (p.h8.codes)
+    return p.y8.codes ? launch_grad_vec<T, 1, 2>(p, stream) : launch_grad_vec<T, 0, 2>(p, stream);
+  return p.y8.codes ? launch_grad_vec<T, 1, 1>(p, stream) : launch_grad_vec<T, 0, 1>(p, stream);
 }
 
 }  // namespace
@@ -802,7 +906,7 @@ int dpopt_block_join(const dpopt_block_join_args* a, dpopt_stream_t stream) {
   p.rstd_post = a->rstd_post;
   p.rstd_pre = a->rstd_pre;
   p.dbg = make_dbg();
-  const bool vec = cols % 8 == 0 && vec_ok(p.h) && vec_ok(p.y) && vec_ok(p.h_out) &&
+  const bool vec = cols % 8 == 0 && cols <= kVecCols && vec_ok(p.h) && vec_ok(p.y) && vec_ok(p.h_out) &&
                    vec_ok(p.u) && vec_ok(p.y8) && vec_ok(p.h8) && vec_ok(p.u8);
   const cudaStream_t st = (cudaStream_t)stream;
   if (a->dtype == DPOPT_GRAD_BF16) return launch_join<bf16>(p, vec, st);
@@ -907,7 +1011,7 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   p.per = part_rows(rows, cols);
   p.parts = parts;
   if (rows > 0) {
-    const bool vec = cols % 8 == 0 && vec_ok(p.dh_out) && vec_ok(p.du) && vec_ok(p.y) &&
+    const bool vec = cols % 8 == 0 && cols <= kVecCols && vec_ok(p.dh_out) && vec_ok(p.du) && vec_ok(p.y) &&
                      vec_ok(p.h_out) && vec_ok(p.dh) && vec_ok(p.dy) && vec_ok(p.y8) &&
                      vec_ok(p.h8);
     const cudaStream_t st = (cudaStream_t)stream;
@@ -920,10 +1024,11 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   // border (none when the parts are whole numbers of gate rows)
   unsigned gate_sums = 0;
   if (p.dgate.data) {
+    p.by_gate = gates <= parts;
     if (a->gate_rows == 0)
       gate_sums = rows == 0 || parts > 1;
-    else if (rows > 0 && part_rows(rows, cols) % a->gate_rows != 0)
-      gate_sums = (unsigned)(parts - 1);
+    else if (rows > 0 && p.per % a->gate_rows != 0)
+      gate_sums = (unsigned)(p.by_gate ? gates : parts - 1);
   }
   if (!p.dw_pre && !p.dw_post && gate_sums == 0) return DPOPT_OK;
   const dim3 grid((unsigned)((cols + 31) / 32), 2 + gate_sums);

@@ -234,8 +234,7 @@ struct Stretch {
 
 // K = 1 .. top largest of the keys a thread can list, by `top` passes over
 // them: each pass takes the largest below the last.  The form for rows whose
-// candidates are too many for the list (few distinct or few unmasked logits)
-// and for joining the parts' lists.
+// candidates are too many for the list (few distinct or few unmasked logits).
 template <class F>
 __device__ __forceinline__ void top_by_passes(int top, uint64_t* best, TokShared& sh, F each) {
   uint64_t last = ~0ull;
@@ -369,7 +368,7 @@ __device__ void finish_row(const LogprobParams& p, int64_t row, const T* x, TokP
 // One CTA per part of a row: one pass with a running softmax per thread, four
 // vectors in flight.
 template <class T>
-__global__ void __launch_bounds__(kTokThreads) token_logprob_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kTokThreads) token_logprob_kernel(const __grid_constant__ LogprobParams p) {
   pdl_enter();
   __shared__ TokShared sh;
   const int64_t row = blockIdx.x / p.parts;
@@ -404,9 +403,11 @@ __global__ void __launch_bounds__(kTokThreads) token_logprob_kernel(const Logpro
   if ((int)threadIdx.x < p.top) p.keys[at * p.top + threadIdx.x] = sh.best[threadIdx.x];
 }
 
-// Joins the parts of a row, one CTA per row.
+// Joins the parts of a row, one CTA per row.  The parts' lists are sorted: one warp
+// holds two lists' heads per lane and takes the largest head `top` times.
 template <class T>
-__global__ void __launch_bounds__(kTokThreads) token_logprob_join_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kTokThreads)
+    token_logprob_join_kernel(const __grid_constant__ LogprobParams p) {
   pdl_enter();
   __shared__ TokShared sh;
   __shared__ uint64_t keys[kTokMaxParts * DPOPT_MAX_TOP];
@@ -415,11 +416,28 @@ __global__ void __launch_bounds__(kTokThreads) token_logprob_join_kernel(const L
   for (int i = threadIdx.x; i < n; i += kTokThreads) keys[i] = p.keys[row * n + i];
   TokPartial t{-INFINITY, -INFINITY, 0.f, 0.f};
   if ((int)threadIdx.x < p.parts) t = p.partial[row * p.parts + threadIdx.x];
-  t = cta_merge(t, sh);
-  if (p.top > 0)
-    top_by_passes(p.top, sh.best, sh, [&](auto take) {
-      for (int i = threadIdx.x; i < n; i += kTokThreads) take(keys[i]);
-    });
+  t = cta_merge(t, sh);  // its barrier also completes `keys`
+  if (p.top > 0) {
+    if (threadIdx.x < 32) {
+      const int l[2] = {(int)threadIdx.x, (int)threadIdx.x + 32};
+      int next[2] = {0, 0};
+      uint64_t head[2];
+      for (int h = 0; h < 2; ++h) head[h] = l[h] < p.parts ? keys[l[h] * p.top] : 0;
+      for (int k = 0; k < p.top; ++k) {
+        uint64_t b = head[0] > head[1] ? head[0] : head[1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t c = __shfl_xor_sync(0xffffffffu, b, o);
+          b = c > b ? c : b;
+        }
+        if (threadIdx.x == 0) sh.best[k] = b;
+        for (int h = 0; h < 2; ++h)
+          if (head[h] == b && b != 0)
+            head[h] = ++next[h] < p.top ? keys[l[h] * p.top + next[h]] : 0;
+      }
+    }
+    __syncthreads();
+  }
   finish_row<T>(p, row, static_cast<const T*>(p.logits) + row * p.ld, t, sh.best, sh);
 }
 
@@ -437,53 +455,63 @@ struct LogprobGradParams {
   Dbg dbg;
 };
 
-// A row is cut into stretches of kGradStretch elements, one CTA each.  Every
-// element gets its share of -p_j; after a barrier the given tokens' elements of
-// the stretch, whose logits were read before (dlogits may be the logits), are
-// stored again with their own terms.  With
+// A row is cut into stretches of kGradStretch elements, one CTA each, four vectors a
+// thread, asked for before anything else.  With
 //   q = (x - m) c - L log2(e)   (the log probability in powers of two)
 // an element is 2^q (A + B q): A = -scale (sum dlogprob + dentropy entropy), B =
-// -scale dentropy ln 2.  q is held above -1e4, where 2^q is 0 in fp32: a masked
-// entry gives 0 and no product overflows.
+// -scale dentropy ln 2, and a given token's element has scale dlogprob more.  q is
+// held above -1e4, where 2^q is 0 in fp32: a masked entry gives 0 and no product
+// overflows.  With one token per row (ONE) its element is met on the way; more
+// are stored again after a barrier, from logits read before it (dlogits may be
+// the logits).
 constexpr int64_t kGradStretch = 4 * kTokThreads * 8;
 
-template <class T>
-__global__ void __launch_bounds__(kTokThreads, 4)
-token_logprob_grad_kernel(const LogprobGradParams p) {
+template <class T, bool ONE>
+__global__ void __launch_bounds__(kTokThreads, 5)
+token_logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
   pdl_enter();
-  __shared__ int64_t tok[DPOPT_MAX_TOKENS];
-  __shared__ float dlp[DPOPT_MAX_TOKENS];
-  __shared__ T given[DPOPT_MAX_TOKENS];
-  const int64_t row = blockIdx.x / p.stretches;
+  __shared__ int64_t tok[ONE ? 1 : DPOPT_MAX_TOKENS];
+  __shared__ float dlp[ONE ? 1 : DPOPT_MAX_TOKENS];
+  __shared__ T given[ONE ? 1 : DPOPT_MAX_TOKENS];
+  const int64_t row = blockIdx.x / (uint32_t)p.stretches;
   const int64_t lo = (blockIdx.x - row * p.stretches) * p.stretch_len;
   const int64_t hi = min(p.vocab, lo + p.stretch_len);
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
   T* out = static_cast<T*>(p.dlogits) + row * p.ld_out;
   const Stretch<T> st(x, lo, hi);
   const T* body = st.x + st.head;
-  // most stretches are four vectors a thread: ask for them before anything else
-  const bool whole = st.vecs >= 4 * kTokThreads;
+  const int vecs = (int)st.vecs;
   Raw8<T> r[4];
-  if (whole)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) r[u] = ld_raw8<T>(body + (threadIdx.x + u * kTokThreads) * 8);
+  for (int u = 0; u < 4; ++u) {
+    const int v = threadIdx.x + u * kTokThreads;
+    if (v < vecs) r[u] = ld_raw8<T>(body + v * 8);
+  }
   const float scale = (p.loss_scale ? p.loss_scale->scale : 1.f) * p.inv_temp;
   const float m = p.stats[row * 2], logsum = p.stats[row * 2 + 1];
   const float dh = p.dentropy ? p.dentropy[row] : 0.f;
   const float ent = p.dentropy ? p.entropy[row] : 0.f;
-  if ((int)threadIdx.x < p.n_tokens) {
-    const int64_t t = p.tokens[row * p.n_tokens + threadIdx.x];
-    tok[threadIdx.x] = t;
-    dlp[threadIdx.x] =
-        t < 0 ? 0.f : t >= p.vocab ? NAN : p.dlogprob[row * p.n_tokens + threadIdx.x];
-    if (t >= lo && t < hi) given[threadIdx.x] = x[t];
-  }
-  __syncthreads();
   float a = 0.f;
-  bool none = true;  // no token given
-  for (int i = 0; i < p.n_tokens; ++i) {
-    a += dlp[i];
-    none = none && tok[i] < 0;
+  bool none = true;   // no token given
+  int64_t one = -1;   // ONE: the token, relative to this stretch's vectors
+  if constexpr (ONE) {
+    const int64_t t = p.tokens[row];
+    none = t < 0;
+    a = t < 0 ? 0.f : t >= p.vocab ? NAN : p.dlogprob[row];
+    one = t < p.vocab ? t - lo : -1;
+  } else {
+    if ((int)threadIdx.x < p.n_tokens) {
+      const int64_t t = p.tokens[row * p.n_tokens + threadIdx.x];
+      tok[threadIdx.x] = t;
+      dlp[threadIdx.x] =
+          t < 0 ? 0.f : t >= p.vocab ? NAN : p.dlogprob[row * p.n_tokens + threadIdx.x];
+      if (t >= lo && t < hi) given[threadIdx.x] = x[t];
+    }
+    __syncthreads();
+    for (int i = 0; i < p.n_tokens; ++i) {
+      a += dlp[i];
+      none = none && tok[i] < 0;
+    }
   }
   constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
   const bool zero = m == -INFINITY || (none && dh == 0.f);
@@ -494,25 +522,40 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
     const float q = max_nan(fmaf(v - m, p.c, -l2), -1e4f);
     return zero ? 0.f : exp2_approx(q) * fmaf(B, q, A);
   };
+  // a given token's own term, unless its entry is masked
+  auto own = [&](float v, float g, float d) { return v == -INFINITY || zero ? g : fmaf(scale, d, g); };
   for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads) {
     const int64_t j = st.loose_at(t);
-    dst[j] = from_f32<T>(grad(to_f32(st.x[j])));
+    const float v = to_f32(st.x[j]);
+    float g = grad(v);
+    if (ONE && j == one) g = own(v, g, a);
+    dst[j] = from_f32<T>(g);
   }
+  one -= st.head;
   const bool vec = ((uintptr_t)(dst + st.head) & 15) == 0;
-  auto eight = [&](const Raw8<T>& r, int64_t v) {
+  const uint64_t c2 = pair(p.c, p.c), m2 = pair(-m, -m), l22 = pair(-l2, -l2);
+  const uint64_t A2 = pair(A, A), B2 = pair(B, B);
+  auto eight = [&](const Raw8<T>& raw, int v) {
     float f[8];
-    widen8<T>(r, f);
-    const uint64_t c2 = pair(p.c, p.c), m2 = pair(-m, -m), l22 = pair(-l2, -l2);
-    const uint64_t A2 = pair(A, A), B2 = pair(B, B);
+    widen8<T>(raw, f);
+    const bool here = ONE && (uint64_t)(one - v * 8) < 8;
+    float at = 0.f;  // the token's logit
+    if (here)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at = one - v * 8 == i ? f[i] : at;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       uint64_t q = fma2(add2(pair(f[i], f[i + 1]), m2), c2, l22);
       q = pair(max_nan(lane0(q), -1e4f), max_nan(lane1(q), -1e4f));
       q = mul2(pair(exp2_approx(lane0(q)), exp2_approx(lane1(q))), fma2(B2, q, A2));
-      f[i] = lane0(q);
-      f[i + 1] = lane1(q);
+      f[i] = zero ? 0.f : lane0(q);
+      f[i + 1] = zero ? 0.f : lane1(q);
     }
-    T* d = dst + st.head + v * 8;
+    if (here)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (one - v * 8 == i) f[i] = own(at, f[i], a);
+    T* d = dst + st.head + (int64_t)v * 8;
     if (vec) {
       st_vec8<T>(d, f);
     } else {
@@ -520,39 +563,26 @@ token_logprob_grad_kernel(const LogprobGradParams p) {
       for (int i = 0; i < 8; ++i) d[i] = from_f32<T>(f[i]);
     }
   };
-  if (zero) {  // nothing to read
-    float f[8] = {};
-    for (int64_t v = threadIdx.x; v < st.vecs; v += kTokThreads) {
-      T* d = dst + st.head + v * 8;
-      if (vec) {
-        st_vec8<T>(d, f);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = from_f32<T>(0.f);
-      }
-    }
-    return;
+  for (int u = 0; u < 4; ++u) {
+    const int v = threadIdx.x + u * kTokThreads;
+    if (v < vecs) eight(r[u], v);
   }
-  int64_t v = threadIdx.x;
-  if (whole) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) eight(r[u], v + u * kTokThreads);
-    v += 4 * kTokThreads;
-  }
-  for (; v < st.vecs; v += kTokThreads) eight(ld_raw8<T>(body + v * 8), v);
-  __syncthreads();
-  if ((int)threadIdx.x < p.n_tokens) {
-    const int64_t t = tok[threadIdx.x];
-    bool mine = t >= lo && t < hi;
-    float own = 0.f;
-    for (int i = 0; i < p.n_tokens; ++i)
-      if (tok[i] == t) {
-        if (i < (int)threadIdx.x) mine = false;  // an equal token before this one stores it
-        own += dlp[i];
+  if constexpr (!ONE) {
+    __syncthreads();
+    if ((int)threadIdx.x < p.n_tokens) {
+      const int64_t t = tok[threadIdx.x];
+      bool mine = t >= lo && t < hi;
+      float d = 0.f;
+      for (int i = 0; i < p.n_tokens; ++i)
+        if (tok[i] == t) {
+          if (i < (int)threadIdx.x) mine = false;  // an equal token before this one stores it
+          d += dlp[i];
+        }
+      if (mine && dbg_ok(p.dbg, t < p.vocab)) {
+        const float v = to_f32(given[threadIdx.x]);
+        out[t] = from_f32<T>(own(v, grad(v), d));
       }
-    if (mine && dbg_ok(p.dbg, t < p.vocab)) {
-      const float v = to_f32(given[threadIdx.x]);
-      out[t] = from_f32<T>(v == -INFINITY ? 0.f : fmaf(scale, own, grad(v)));
     }
   }
 }
@@ -728,9 +758,15 @@ int dpopt_token_logprob_backward(const void* logits, int dtype, int64_t rows, in
   p.dlogits = dlogits;
   p.dbg = make_dbg();
   if (rows > INT32_MAX / p.stretches) return fail(DPOPT_ERR_UNSUPPORTED, "too many rows");
-  auto kern = dtype == DPOPT_GRAD_BF16  ? token_logprob_grad_kernel<bf16>
-              : dtype == DPOPT_GRAD_F16 ? token_logprob_grad_kernel<fp16>
-                                        : token_logprob_grad_kernel<float>;
+  const bool one = n_tokens == 1;
+  auto kern = dtype == DPOPT_GRAD_BF16
+                  ? (one ? token_logprob_grad_kernel<bf16, true>
+                         : token_logprob_grad_kernel<bf16, false>)
+              : dtype == DPOPT_GRAD_F16
+                  ? (one ? token_logprob_grad_kernel<fp16, true>
+                         : token_logprob_grad_kernel<fp16, false>)
+                  : (one ? token_logprob_grad_kernel<float, true>
+                         : token_logprob_grad_kernel<float, false>);
   return launched(launch_pdl(kern, (unsigned)(rows * p.stretches), kTokThreads, 0,
                              (cudaStream_t)stream, p),
                   "token logprob gradient");
