@@ -66,17 +66,35 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr
 // Values of a parameter (row `at` elements in; ones where it is absent) at a
 // thread's columns, into its places out[i * stride].  Not inlined: parameters are
 // read once per launch or gate row, and their three types and eight addresses
-// would take the registers of the loops around it.
+// would take the registers of the loops around it.  All the loads come before the
+// first conversion or store, so that they are in flight together.
+template <class W, bool VEC, int NV>
+__device__ __forceinline__ void stage_typed(const W* w, int t, int tpr, int cols, float* out,
+                                            int stride) {
+  W raw[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[v][i] = w[min(column<VEC>(v, i, t, tpr), cols - 1)];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[(v * 8 + i) * stride] = to_f32(raw[v][i]);
+}
+
 template <bool VEC, int NV>
 __device__ __noinline__ void stage_param(const void* w, int dtype, int64_t at, int t, int tpr,
                                          int cols, float* out, int stride) {
-#pragma unroll 1
-  for (int v = 0; v < NV; ++v)
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(v, i, t, tpr);
-      out[(v * 8 + i) * stride] = w && c < cols ? ld_any(w, dtype, at + c) : 1.f;
-    }
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < NV * 8; ++i) out[i * stride] = 1.f;
+  } else if (dtype == DPOPT_GRAD_BF16) {
+    stage_typed<bf16, VEC, NV>(static_cast<const bf16*>(w) + at, t, tpr, cols, out, stride);
+  } else if (dtype == DPOPT_GRAD_F16) {
+    stage_typed<fp16, VEC, NV>(static_cast<const fp16*>(w) + at, t, tpr, cols, out, stride);
+  } else {
+    stage_typed<float, VEC, NV>(static_cast<const float*>(w) + at, t, tpr, cols, out, stride);
+  }
 }
 
 __host__ __device__ inline int64_t gate_row_of(int64_t gate_rows, int64_t row) {
@@ -515,6 +533,38 @@ struct ElemRows {
 
 // At the end of a gate row's rows in a part: its sums branch_scale * e (in `mine`)
 // go into dw_post's and into dgate, or into a partial row of it.
+template <class W, bool VEC, int NV>
+__device__ __forceinline__ void close_typed(const JoinGradParams& p, bool inside, int64_t grow,
+                                            float* out, int t, float* post, const float* mine,
+                                            int stride) {
+  const W* gate = p.gate.data ? static_cast<const W*>(p.gate.data) + grow * p.gate.ld : nullptr;
+  const W* wpost = static_cast<const W*>(p.w_post);
+  W g[NV][8], w[NV][8];  // read before the first conversion or store
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(column<VEC>(v, i, t, p.tpr), p.cols - 1);
+      g[v][i] = gate ? gate[c] : from_f32<W>(1.f);
+      w[v][i] = wpost ? wpost[c] : from_f32<W>(1.f);
+    }
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<VEC>(v, i, t, p.tpr);
+      if (c >= p.cols) continue;
+      float& sum = post[(v * 8 + i) * stride];
+      const float x = mine[(v * 8 + i) * stride];
+      sum = fmaf(to_f32(g[v][i]), x, sum);
+      if (!p.dgate.data) continue;
+      if (inside)
+        (static_cast<W*>(p.dgate.data) + grow * p.dgate.ld)[c] = from_f32<W>(to_f32(w[v][i]) * x);
+      else
+        out[c] = to_f32(w[v][i]) * x;
+    }
+}
+
 template <bool VEC, int NV>
 __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t part, int64_t lo,
                                             int64_t hi, int64_t row, bool first_gate, int t,
@@ -524,22 +574,12 @@ __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t par
   const bool inside = glo >= lo && ghi <= hi;
   const int64_t grow = gate_row_of(p.gate_rows, row);
   float* out = part_row(p, part, first_gate ? kPartGateFirst : kPartGateLast);
-#pragma unroll 1
-  for (int v = 0; v < NV; ++v)
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(v, i, t, p.tpr);
-      if (c >= p.cols) continue;
-      const float x = mine[(v * 8 + i) * stride];
-      const float g = p.gate.data ? ld_any(p.gate.data, p.param_dtype, grow * p.gate.ld + c) : 1.f;
-      const float w = p.w_post ? ld_any(p.w_post, p.param_dtype, c) : 1.f;
-      post[(v * 8 + i) * stride] = fmaf(g, x, post[(v * 8 + i) * stride]);
-      if (!p.dgate.data) continue;
-      if (inside)
-        st_any(p.dgate.data, p.param_dtype, grow * p.dgate.ld + c, w * x);
-      else
-        out[c] = w * x;
-    }
+  if (p.param_dtype == DPOPT_GRAD_BF16)
+    close_typed<bf16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+  else if (p.param_dtype == DPOPT_GRAD_F16)
+    close_typed<fp16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+  else
+    close_typed<float, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
 }
 
 // One CTA per run of rows.  Per row one reading forms three sums,
