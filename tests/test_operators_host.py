@@ -45,6 +45,37 @@ def test_argument_blocks_match_the_header(dp, tmp_path):
         assert int(value) == (ctypes.sizeof(py) if field == "size" else getattr(py, field).offset)
 
 
+def test_packed_argument_layouts_match_the_blocks(dp):
+    """The wrappers pack the argument blocks with struct formats: the same sizes and, field
+    by field, the same bytes as the ctypes structures."""
+    for fmt, py in ((dp.operators._JOIN, dp.binding.BlockJoinArgs),
+                    (dp.operators._JOIN_GRAD, dp.binding.BlockJoinGradArgs)):
+        assert fmt.size == ctypes.sizeof(py)
+        values = []
+
+        def leaves(kind):
+            for _, t in kind._fields_:
+                if hasattr(t, "_fields_"):
+                    leaves(t)
+                else:
+                    v = len(values) + 1
+                    values.append(float(v) if t is ctypes.c_float else v)
+
+        leaves(py)
+        raw = fmt.pack(*values)
+        obj, it = py.from_buffer_copy(raw), iter(values)
+
+        def check(o):
+            for n, t in o._fields_:
+                x = getattr(o, n)
+                if hasattr(t, "_fields_"):
+                    check(x)
+                else:
+                    assert x == next(it), n
+
+        check(obj)
+
+
 # fake, never-dereferenced device addresses
 A = [0x10_0000_0000 + i * 0x1_0000_0000 for i in range(32)]
 

@@ -173,8 +173,8 @@ _SIGS = {
     "dpopt_act8_wgrad": ([_P, _I, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I, _I64, _P,
                           _I64, _P, _I64, _P], _I),
     "dpopt_act8_wgrad_scratch_bytes": ([_I64, _I64, _I64, _PI64], _I),
-    "dpopt_block_join": ([ctypes.POINTER(BlockJoinArgs), _P], _I),
-    "dpopt_block_join_backward": ([ctypes.POINTER(BlockJoinGradArgs), _P], _I),
+    "dpopt_block_join": ([_P, _P], _I),
+    "dpopt_block_join_backward": ([_P, _P], _I),
     "dpopt_block_join_scratch_bytes": ([_I64, _I64, _I64, _PI64], _I),
     "dpopt_token_logprob": ([_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _I, _P, _P, _P,
                              _I64, _P], _I),

@@ -629,11 +629,9 @@ int encode(CUtensorMap* map, bool is_bf16, const void* base, int64_t cols, int64
 template <class T, int CG, int BN>
 int launch_gemm(const GemmParams& p, const CUtensorMap& a, const CUtensorMap& b,
                 cudaStream_t stream) {
-  auto kern = act8_wgrad_kernel<T, CG, BN>;
+  constexpr auto kern = act8_wgrad_kernel<T, CG, BN>;
   const size_t smem = GemmShape<CG, BN>::kSmem;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_fail(e, "shared memory size");
+  DPOPT_TRY(allow_smem<kern>(smem));
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;

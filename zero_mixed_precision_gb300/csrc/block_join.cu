@@ -1,6 +1,7 @@
 // block_join.cu -- the join between two transformer blocks (the norm after the
 // block, gate, residual scale, the norm before the next block) and its
 // gradient; the formulas stand in include/dpopt.h.
+#include <atomic>
 #include <cmath>
 
 #include "ops.cuh"
@@ -824,25 +825,25 @@ bool vec_ok(const Act8Out& a) { return !a.codes || a.vec; }
 
 constexpr size_t kJoinSmem = 220 * 1024;  // of 227 KB; the static arrays need some
 
-template <class K>
-int allow_smem(K kern, size_t bytes) {
-  if (bytes <= 40 * 1024) return DPOPT_OK;  // 48 KB without asking, static arrays included
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  return e == cudaSuccess ? DPOPT_OK : cuda_fail(e, "shared memory size");
-}
-
 template <class T, bool VEC, int NV>
 int launch_join_at(JoinParams& p, cudaStream_t stream) {
-  auto kern = block_join_kernel<T, VEC, NV>;
-  int sms = 0, per_sm = 0;
+  constexpr auto kern = block_join_kernel<T, VEC, NV>;
+  int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const size_t smem = (size_t)p.tpr * 8 * NV * sizeof(float);
-  DPOPT_TRY(allow_smem(kern, smem));
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.tpr, smem);
-  if (e != cudaSuccess) return cuda_fail(e, "block join occupancy");
-  const unsigned grid =
-      (unsigned)std::min<int64_t>(p.rows, (int64_t)sms * std::max(per_sm, 1));
+  DPOPT_TRY(allow_smem<kern>(smem));
+  // CTAs an SM holds, asked once per CTA size
+  static std::atomic<int> resident[kJoinCta / 32 + 1];
+  std::atomic<int>& held = resident[p.tpr / 32];
+  int per_sm = held.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    const cudaError_t e =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.tpr, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "block join occupancy");
+    per_sm = std::max(per_sm, 1);
+    held.store(per_sm, std::memory_order_relaxed);
+  }
+  const unsigned grid = (unsigned)std::min<int64_t>(p.rows, (int64_t)sms * per_sm);
   return launched(launch_pdl(kern, grid, p.tpr, smem, stream, p), "block join");
 }
 
@@ -855,11 +856,11 @@ int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
 
 template <class T, bool VEC, class Rows>
 int launch_grad_at(JoinGradParams& p, size_t room, cudaStream_t stream) {
-  auto kern = block_join_grad_kernel<T, VEC, Rows>;
+  constexpr auto kern = block_join_grad_kernel<T, VEC, Rows>;
   const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
   p.stages = VEC ? (int)std::min<size_t>(3, (room - sums) / p.stage_bytes) : 0;
   const size_t smem = sums + (size_t)p.stages * p.stage_bytes;
-  DPOPT_TRY(allow_smem(kern, smem));
+  DPOPT_TRY(allow_smem<kern>(smem));
   return launched(launch_pdl(kern, (unsigned)p.parts, p.tpr, smem, stream, p),
                   "block join gradient");
 }

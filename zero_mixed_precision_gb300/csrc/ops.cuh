@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -448,6 +449,27 @@ inline int take_act8(const char* name, const dpopt_act8& a, int64_t rows, int64_
   ++*n;
   *out = Act8Out{a.codes, a.ld_codes, a.exps, a.ld_exps,
                  (uintptr_t)a.codes % 8 == 0 && (rows <= 1 || a.ld_codes % 8 == 0)};
+  return DPOPT_OK;
+}
+
+// Lets KERN use `bytes` of dynamic shared memory on the current device; asked of
+// the driver once per device and size.
+template <auto KERN>
+int allow_smem(size_t bytes) {
+  constexpr int kDevices = 64;
+  static std::atomic<size_t> granted[kDevices];
+  if (bytes <= 40 * 1024) return DPOPT_OK;  // 48 KB without asking, static arrays included
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < kDevices && granted[dev].load(std::memory_order_relaxed) >= bytes) return DPOPT_OK;
+  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "shared memory size");
+  if (dev < kDevices) {
+    size_t was = granted[dev].load(std::memory_order_relaxed);
+    while (was < bytes && !granted[dev].compare_exchange_weak(was, bytes)) {
+    }
+  }
   return DPOPT_OK;
 }
 

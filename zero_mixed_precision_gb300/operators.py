@@ -11,48 +11,87 @@ tensors must belong like those of any kernel launched there.
 """
 from __future__ import annotations
 
+import struct
+
 from .binding import (
-    Act8, BlockJoinArgs, BlockJoinGradArgs, Matrix, _check, _grad_dtype, _operand, _stream_handle,
-    dpopt_act8_pack, dpopt_act8_unpack, dpopt_act8_wgrad, dpopt_act8_wgrad_scratch_bytes,
-    dpopt_block_join, dpopt_block_join_backward, dpopt_block_join_scratch_bytes,
-    dpopt_token_logprob, dpopt_token_logprob_backward, dpopt_token_logprob_scratch_bytes,
+    DPOPT_GRAD_BF16, DPOPT_GRAD_F16, DPOPT_GRAD_F32, _check, _lib, _operand,
+    dpopt_act8_wgrad_scratch_bytes, dpopt_block_join_scratch_bytes,
+    dpopt_token_logprob_scratch_bytes,
 )
 
 ACT8_BLOCK = 32
 
+# dpopt_block_join_args and dpopt_block_join_grad_args as bytes: a call packs its
+# numbers in one go (ctypes structures, field by field, took most of a small
+# call's time)
+_JOIN = struct.Struct("@qqiifffiq" + "Pq" * 5 + "PPPP" + "PqPq" * 3)
+_JOIN_GRAD = struct.Struct("@qqiiffq" + "Pq" * 8 + "PqPq" * 2 + "P" * 7 + "q")
+_NO_MATRIX = (0, 0)
+_NO_ACT8 = (0, 0, 0, 0)
 
-def _want(t, name: str, shape, dtype=None) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+_torch = None
+_types: dict = {}
+
+
+def _load():
+    """torch, imported at the first call, and the dtype codes."""
+    global _torch
+    if _torch is None:
+        import torch
+        _types.update({torch.bfloat16: DPOPT_GRAD_BF16, torch.float16: DPOPT_GRAD_F16,
+                       torch.float32: DPOPT_GRAD_F32})
+        _torch = torch
+    return _torch
+
+
+def _dtype(t, name: str) -> int:
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}") from None
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        return _torch.cuda.current_stream().cuda_stream
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 def _address(t) -> int:
+    if t.is_cuda:
+        return t.data_ptr()
     return _operand(t) if t.numel() else 0
+
+
+def _mismatch(t, name: str, shape, dtype):
+    if tuple(t.shape) != tuple(shape):
+        return ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return TypeError(f"{name}: {t.dtype}, expected {dtype}")
 
 
 def _matrix(t, name: str, shape, dtype=None) -> tuple[int, int]:
     """Address and row stride of a 2-D tensor with adjacent columns."""
-    _want(t, name, shape, dtype)
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: columns must be adjacent (column stride {t.stride(1)})")
-    return _address(t), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
+        raise _mismatch(t, name, shape, dtype)
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1 and shape[0] > 0:
+        raise ValueError(f"{name}: columns must be adjacent (column stride {step})")
+    return _address(t), ld if shape[0] > 1 else shape[1]
 
 
 def _flat(t, name: str, shape, dtype) -> int:
     """Address of a contiguous tensor."""
-    _want(t, name, shape, dtype)
+    if t.shape != shape or t.dtype != dtype:
+        raise _mismatch(t, name, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return _address(t)
 
 
 def _packed(pair, name: str, rows: int, cols: int) -> tuple[int, int, int, int]:
-    import torch
     codes, exps = pair
-    return (*_matrix(codes, f"{name} codes", (rows, cols), torch.int8),
-            *_matrix(exps, f"{name} exps", (rows, -(-cols // ACT8_BLOCK)), torch.uint8))
+    return (*_matrix(codes, f"{name} codes", (rows, cols), _torch.int8),
+            *_matrix(exps, f"{name} exps", (rows, -(-cols // ACT8_BLOCK)), _torch.uint8))
 
 
 def _scratch(t) -> tuple[int, int]:
@@ -63,35 +102,38 @@ def _scratch(t) -> tuple[int, int]:
     return _address(t), t.numel() * t.element_size()
 
 
-def _rows_cols(t, name: str) -> tuple[int, int]:
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got {t.dim()}")
-    return t.shape[0], t.shape[1]
+def _rows_cols(t, name: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got {len(shape)}")
+    return shape
 
 
 def act8_empty(rows: int, cols: int, device="cuda"):
     """Storage for a packed rows x cols matrix: (codes, exps), uninitialised."""
-    import torch
-    return (torch.empty(rows, cols, dtype=torch.int8, device=device),
-            torch.empty(rows, -(-cols // ACT8_BLOCK), dtype=torch.uint8, device=device))
+    torch = _load()
+    return (torch.empty((rows, cols), dtype=torch.int8, device=device),
+            torch.empty((rows, -(-cols // ACT8_BLOCK)), dtype=torch.uint8, device=device))
 
 
 def act8_pack(x, codes, exps, stream=None) -> None:
     """Pack x (bf16, fp16 or fp32) into 8-bit codes and one exponent byte per 32 columns."""
-    rows, cols = _rows_cols(x, "x")
-    px, ldx = _matrix(x, "x", (rows, cols))
+    _load()
+    rows, cols = shape = _rows_cols(x, "x")
+    px, ldx = _matrix(x, "x", shape)
     c, ldc, e, lde = _packed((codes, exps), "packed", rows, cols)
-    _check(dpopt_act8_pack(px, _grad_dtype(x), rows, cols, ldx, c, ldc, e, lde,
-                           _stream_handle(stream)), "dpopt_act8_pack")
+    _check(_lib.dpopt_act8_pack(px, _dtype(x, "x"), rows, cols, ldx, c, ldc, e, lde,
+                                _stream(stream)), "dpopt_act8_pack")
 
 
 def act8_unpack(codes, exps, x, stream=None) -> None:
     """Write the packed matrix's values to x."""
-    rows, cols = _rows_cols(x, "x")
-    px, ldx = _matrix(x, "x", (rows, cols))
+    _load()
+    rows, cols = shape = _rows_cols(x, "x")
+    px, ldx = _matrix(x, "x", shape)
     c, ldc, e, lde = _packed((codes, exps), "packed", rows, cols)
-    _check(dpopt_act8_unpack(c, ldc, e, lde, rows, cols, px, _grad_dtype(x), ldx,
-                             _stream_handle(stream)), "dpopt_act8_unpack")
+    _check(_lib.dpopt_act8_unpack(c, ldc, e, lde, rows, cols, px, _dtype(x, "x"), ldx,
+                                  _stream(stream)), "dpopt_act8_unpack")
 
 
 def act8_wgrad_scratch_bytes(tokens: int, n: int, k: int) -> int:
@@ -104,15 +146,17 @@ def act8_wgrad(dy, codes, exps, dw, scratch=None, *, addend=None, stream=None) -
     """dw (n x k) = dy^T X (+ addend): the weight gradient of y = x W^T from dy (tokens x n,
     bf16 or fp16) and the packed x (tokens x k).  addend: a matrix like dw, or dw itself.
     scratch: a device tensor of act8_wgrad_scratch_bytes(tokens, n, k) bytes."""
-    tokens, n = _rows_cols(dy, "dy")
+    _load()
+    tokens, n = shape = _rows_cols(dy, "dy")
     k = _rows_cols(codes, "codes")[1]
-    pdy, lddy = _matrix(dy, "dy", (tokens, n))
+    pdy, lddy = _matrix(dy, "dy", shape)
     c, ldc, e, lde = _packed((codes, exps), "packed", tokens, k)
     pdw, lddw = _matrix(dw, "dw", (n, k))
-    pa, lda = (0, 0) if addend is None else _matrix(addend, "addend", (n, k), dw.dtype)
-    _check(dpopt_act8_wgrad(pdy, _grad_dtype(dy), lddy, c, ldc, e, lde, tokens, n, k, pdw,
-                            _grad_dtype(dw), lddw, pa, lda, *_scratch(scratch),
-                            _stream_handle(stream)), "dpopt_act8_wgrad")
+    pa, lda = _NO_MATRIX if addend is None else _matrix(addend, "addend", (n, k), dw.dtype)
+    ps, ns = _scratch(scratch)
+    _check(_lib.dpopt_act8_wgrad(pdy, _dtype(dy, "dy"), lddy, c, ldc, e, lde, tokens, n, k, pdw,
+                                 _dtype(dw, "dw"), lddw, pa, lda, ps, ns, _stream(stream)),
+           "dpopt_act8_wgrad")
 
 
 def block_join_scratch_bytes(rows: int, cols: int, gate_rows: int = 0) -> int:
@@ -121,12 +165,18 @@ def block_join_scratch_bytes(rows: int, cols: int, gate_rows: int = 0) -> int:
     return nbytes
 
 
-def _param_dtype(tensors, default) -> int:
+def _param_dtype(default, *tensors) -> int:
     """The one type of the weights and gates given."""
-    kinds = {t.dtype for t in tensors if t is not None}
-    if len(kinds) > 1:
-        raise TypeError(f"weights, gates and their gradients must share one type, got {kinds}")
-    return _grad_dtype(next(t for t in tensors if t is not None)) if kinds else default
+    kind = None
+    for t in tensors:
+        if t is None:
+            continue
+        if kind is None:
+            kind = t
+        elif t.dtype != kind.dtype:
+            raise TypeError("weights, gates and their gradients must share one type, got "
+                            f"{kind.dtype} and {t.dtype}")
+    return default if kind is None else _dtype(kind, "weights")
 
 
 def _gate_shape(rows: int, cols: int, gate_rows: int) -> tuple[int, int]:
@@ -144,29 +194,24 @@ def block_join(h, y, h_out, *, eps: float, rstd_post=None, w_post=None, gate=Non
     rows, written (rstd_post None: no norm after the block; u None: none before the next).
     gate: one row for all rows (gate_rows 0) or one for each run of gate_rows rows.  y8,
     h8, u8: packed matrices that receive the 8-bit checkpoints of y, h_out and u."""
-    import torch
-    rows, cols = _rows_cols(h, "h")
-    dt = h.dtype
-    a = BlockJoinArgs(rows=rows, cols=cols, dtype=_grad_dtype(h),
-                      param_dtype=_param_dtype((w_post, w_pre, gate), _grad_dtype(h)), eps=eps,
-                      res_scale=res_scale, branch_scale=branch_scale, gate_rows=gate_rows)
-    a.h = Matrix(*_matrix(h, "h", (rows, cols)))
-    a.y = Matrix(*_matrix(y, "y", (rows, cols), dt))
-    a.h_out = Matrix(*_matrix(h_out, "h_out", (rows, cols), dt))
-    if u is not None:
-        a.u = Matrix(*_matrix(u, "u", (rows, cols), dt))
-    if gate is not None:
-        a.gate = Matrix(*_matrix(gate, "gate", _gate_shape(rows, cols, gate_rows)))
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            setattr(a, name, _flat(t, name, (cols,), t.dtype))
-    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
-        if t is not None:
-            setattr(a, name, _flat(t, name, (rows,), torch.float32))
-    for name, pair in (("y8", y8), ("h8", h8), ("u8", u8)):
-        if pair is not None:
-            setattr(a, name, Act8(*_packed(pair, name, rows, cols)))
-    _check(dpopt_block_join(a, _stream_handle(stream)), "dpopt_block_join")
+    f32 = _load().float32
+    rows, cols = shape = _rows_cols(h, "h")
+    dt, kind = h.dtype, _dtype(h, "h")
+    args = _JOIN.pack(
+        rows, cols, kind, _param_dtype(kind, w_post, w_pre, gate), eps, res_scale, branch_scale, 0,
+        gate_rows, *_matrix(h, "h", shape), *_matrix(y, "y", shape, dt),
+        *(_NO_MATRIX if gate is None else
+          _matrix(gate, "gate", _gate_shape(rows, cols, gate_rows))),
+        *_matrix(h_out, "h_out", shape, dt),
+        *(_NO_MATRIX if u is None else _matrix(u, "u", shape, dt)),
+        0 if w_post is None else _flat(w_post, "w_post", (cols,), w_post.dtype),
+        0 if w_pre is None else _flat(w_pre, "w_pre", (cols,), w_pre.dtype),
+        0 if rstd_post is None else _flat(rstd_post, "rstd_post", (rows,), f32),
+        0 if rstd_pre is None else _flat(rstd_pre, "rstd_pre", (rows,), f32),
+        *(_NO_ACT8 if y8 is None else _packed(y8, "y8", rows, cols)),
+        *(_NO_ACT8 if h8 is None else _packed(h8, "h8", rows, cols)),
+        *(_NO_ACT8 if u8 is None else _packed(u8, "u8", rows, cols)))
+    _check(_lib.dpopt_block_join(args, _stream(stream)), "dpopt_block_join")
 
 
 def block_join_backward(dh_out, y, dy, dh, scratch, *, rstd_post=None, w_post=None, dw_post=None,
@@ -178,36 +223,37 @@ def block_join_backward(dh_out, y, dy, dh, scratch, *, rstd_post=None, w_post=No
     checkpoints (codes, exps); rstd_post and rstd_pre are those it stored.  du None: the
     join had no norm before the next block.  scratch: a device tensor of
     block_join_scratch_bytes(rows, cols, gate_rows) bytes."""
-    import torch
-    rows, cols = _rows_cols(dh_out, "dh_out")
-    dt = dh_out.dtype
-    a = BlockJoinGradArgs(
-        rows=rows, cols=cols, dtype=_grad_dtype(dh_out),
-        param_dtype=_param_dtype((w_post, w_pre, gate, dw_post, dw_pre, dgate),
-                                 _grad_dtype(dh_out)),
-        res_scale=res_scale, branch_scale=branch_scale, gate_rows=gate_rows)
-    a.dh_out = Matrix(*_matrix(dh_out, "dh_out", (rows, cols)))
-    a.dy = Matrix(*_matrix(dy, "dy", (rows, cols), dt))
-    for name, t in (("dh", dh), ("du", du)):
-        if t is not None:
-            setattr(a, name, Matrix(*_matrix(t, name, (rows, cols), dt)))
-    for name, eight, t in (("y", "y8", y), ("h_out", "h8", h_out)):
-        if isinstance(t, (tuple, list)):
-            setattr(a, eight, Act8(*_packed(t, name, rows, cols)))
-        elif t is not None:
-            setattr(a, name, Matrix(*_matrix(t, name, (rows, cols), dt)))
-    for name, t in (("gate", gate), ("dgate", dgate)):
-        if t is not None:
-            setattr(a, name, Matrix(*_matrix(t, name, _gate_shape(rows, cols, gate_rows))))
-    for name, t in (("w_post", w_post), ("w_pre", w_pre), ("dw_post", dw_post),
-                    ("dw_pre", dw_pre)):
-        if t is not None:
-            setattr(a, name, _flat(t, name, (cols,), t.dtype))
-    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
-        if t is not None:
-            setattr(a, name, _flat(t, name, (rows,), torch.float32))
-    a.scratch, a.scratch_bytes = _scratch(scratch)
-    _check(dpopt_block_join_backward(a, _stream_handle(stream)), "dpopt_block_join_backward")
+    f32 = _load().float32
+    rows, cols = shape = _rows_cols(dh_out, "dh_out")
+    dt, kind = dh_out.dtype, _dtype(dh_out, "dh_out")
+    my, y8 = _NO_MATRIX, _NO_ACT8
+    if isinstance(y, (tuple, list)):
+        y8 = _packed(y, "y", rows, cols)
+    else:
+        my = _matrix(y, "y", shape, dt)
+    mh, h8 = _NO_MATRIX, _NO_ACT8
+    if isinstance(h_out, (tuple, list)):
+        h8 = _packed(h_out, "h_out", rows, cols)
+    elif h_out is not None:
+        mh = _matrix(h_out, "h_out", shape, dt)
+    gates = _gate_shape(rows, cols, gate_rows)
+
+    def weight(t, name):
+        return 0 if t is None else _flat(t, name, (cols,), t.dtype)
+
+    args = _JOIN_GRAD.pack(
+        rows, cols, kind, _param_dtype(kind, w_post, w_pre, gate, dw_post, dw_pre, dgate),
+        res_scale, branch_scale, gate_rows, *_matrix(dh_out, "dh_out", shape),
+        *(_NO_MATRIX if du is None else _matrix(du, "du", shape, dt)), *my, *mh,
+        *(_NO_MATRIX if gate is None else _matrix(gate, "gate", gates)),
+        *(_NO_MATRIX if dh is None else _matrix(dh, "dh", shape, dt)),
+        *_matrix(dy, "dy", shape, dt),
+        *(_NO_MATRIX if dgate is None else _matrix(dgate, "dgate", gates)), *y8, *h8,
+        weight(w_post, "w_post"), weight(w_pre, "w_pre"),
+        0 if rstd_post is None else _flat(rstd_post, "rstd_post", (rows,), f32),
+        0 if rstd_pre is None else _flat(rstd_pre, "rstd_pre", (rows,), f32),
+        weight(dw_post, "dw_post"), weight(dw_pre, "dw_pre"), *_scratch(scratch))
+    _check(_lib.dpopt_block_join_backward(args, _stream(stream)), "dpopt_block_join_backward")
 
 
 def token_logprob_scratch_bytes(rows: int, vocab: int, top: int = 0) -> int:
@@ -224,22 +270,23 @@ def token_logprob(logits, tokens, logprob, stats, scratch=None, *, entropy=None,
     gradient); optionally entropy (float32 rows) and the largest alternatives, top_logprob
     (float32) and top_index (int64), rows x top.  scratch: a device tensor of
     token_logprob_scratch_bytes(rows, vocab, top) bytes."""
-    import torch
-    rows, vocab = _rows_cols(logits, "logits")
+    torch = _load()
+    f32, i64 = torch.float32, torch.int64
+    rows, vocab = shape = _rows_cols(logits, "logits")
     n = _rows_cols(tokens, "tokens")[1]
-    px, ld = _matrix(logits, "logits", (rows, vocab))
+    px, ld = _matrix(logits, "logits", shape)
     if (top_logprob is None) != (top_index is None):
         raise ValueError("top_logprob and top_index must be given together")
     top = 0 if top_index is None else _rows_cols(top_index, "top_index")[1]
-    f32 = torch.float32
-    _check(dpopt_token_logprob(
-        px, _grad_dtype(logits), rows, vocab, ld, _flat(tokens, "tokens", (rows, n), torch.int64),
-        n, inv_temperature, _flat(logprob, "logprob", (rows, n), f32),
+    ps, ns = _scratch(scratch)
+    _check(_lib.dpopt_token_logprob(
+        px, _dtype(logits, "logits"), rows, vocab, ld, _flat(tokens, "tokens", (rows, n), i64), n,
+        inv_temperature, _flat(logprob, "logprob", (rows, n), f32),
         _flat(stats, "stats", (rows, 2), f32),
         0 if entropy is None else _flat(entropy, "entropy", (rows,), f32), top,
         0 if top == 0 else _flat(top_logprob, "top_logprob", (rows, top), f32),
-        0 if top == 0 else _flat(top_index, "top_index", (rows, top), torch.int64),
-        *_scratch(scratch), _stream_handle(stream)), "dpopt_token_logprob")
+        0 if top == 0 else _flat(top_index, "top_index", (rows, top), i64), ps, ns,
+        _stream(stream)), "dpopt_token_logprob")
 
 
 def token_logprob_backward(logits, tokens, stats, dlogits, *, dlogprob, entropy=None,
@@ -248,19 +295,19 @@ def token_logprob_backward(logits, tokens, stats, dlogits, *, dlogprob, entropy=
     """dlogits (may be logits) = the gradient of sum(dlogprob * logprob) + sum(dentropy *
     entropy), times the current scale of `loss_scale` (the device state of
     loss_scale_init(); None: 1).  stats and entropy are those token_logprob stored."""
-    import torch
-    rows, vocab = _rows_cols(logits, "logits")
-    n = _rows_cols(tokens, "tokens")[1]
-    px, ld = _matrix(logits, "logits", (rows, vocab))
-    pd, ldd = _matrix(dlogits, "dlogits", (rows, vocab), logits.dtype)
+    torch = _load()
     f32 = torch.float32
+    rows, vocab = shape = _rows_cols(logits, "logits")
+    n = _rows_cols(tokens, "tokens")[1]
+    px, ld = _matrix(logits, "logits", shape)
+    pd, ldd = _matrix(dlogits, "dlogits", shape, logits.dtype)
     if loss_scale is not None and loss_scale.numel() * loss_scale.element_size() < 32:
         raise ValueError("loss_scale: the state is 32 bytes")
-    _check(dpopt_token_logprob_backward(
-        px, _grad_dtype(logits), rows, vocab, ld, _flat(tokens, "tokens", (rows, n), torch.int64),
-        n, inv_temperature, _flat(stats, "stats", (rows, 2), f32),
-        _flat(dlogprob, "dlogprob", (rows, n), f32),
+    _check(_lib.dpopt_token_logprob_backward(
+        px, _dtype(logits, "logits"), rows, vocab, ld,
+        _flat(tokens, "tokens", (rows, n), torch.int64), n, inv_temperature,
+        _flat(stats, "stats", (rows, 2), f32), _flat(dlogprob, "dlogprob", (rows, n), f32),
         0 if entropy is None else _flat(entropy, "entropy", (rows,), f32),
         0 if dentropy is None else _flat(dentropy, "dentropy", (rows,), f32),
-        0 if loss_scale is None else _operand(loss_scale), pd, ldd, _stream_handle(stream)),
+        0 if loss_scale is None else _address(loss_scale), pd, ldd, _stream(stream)),
         "dpopt_token_logprob_backward")
