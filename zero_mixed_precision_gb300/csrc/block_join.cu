@@ -290,6 +290,15 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // kH); begin() and end() stand around each row.
 enum { kDh = 0, kDu = 1, kY = 2, kH = 3 };
 
+// Eight floats of four pairs.
+__device__ __forceinline__ void lanes8(const uint64_t (&f)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = lane0(f[i]);
+    x[2 * i + 1] = lane1(f[i]);
+  }
+}
+
 // Vector form.  Rows come through a ring in shared memory: each thread copies
 // (cp.async) and reads only its own fragments, so that up to three rows are in
 // flight without registers and without barriers.  YP: y comes packed; HP: h_out
@@ -435,33 +444,38 @@ struct VecRows {
       asm volatile("cp.async.wait_group 2;" ::: "memory");
   }
   template <int WHICH>
-  __device__ __forceinline__ void get(int v, float (&f)[8]) const {
+  __device__ __forceinline__ void get(int v, uint64_t (&f)[4]) const {
     constexpr bool none = HP == 0 && (WHICH == kDu || WHICH == kH);
     constexpr bool narrow = (WHICH == kY && YP) || (WHICH == kH && HP == 2);
     if constexpr (none) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      for (int i = 0; i < 4; ++i) f[i] = 0;
     } else if constexpr (narrow) {
       uint2 k;
       asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
                    : "=r"(k.x), "=r"(k.y)
                    : "r"(at[WHICH] + stage * p.stage_bytes + v * tpr * kNarrow)
                    : "memory");
-      act8_values(k, WHICH == kY ? y_scale[v] : h_scale[v], f);
+      act8_pairs(k, WHICH == kY ? y_scale[v] : h_scale[v], f);
     } else {
       const uint32_t a = at[WHICH] + stage * p.stage_bytes + v * tpr * kWide;
       Raw8<T> r;
       r.v = ld_shared16(a);
       if constexpr (sizeof(T) == 4) r.w = ld_shared16(a + 16);
-      widen8<T>(r, f);
+      widen_pairs<T>(r, f);
     }
   }
   __device__ __forceinline__ bool wants_dh() const { return dh_out != nullptr; }
-  __device__ __forceinline__ void put_dh(int v, const float (&f)[8]) const {
-    if (on[v]) st_vec8<T>(dh_out + c[v], f);
+  __device__ __forceinline__ void put_dh(int v, const uint64_t (&f)[4]) const {
+    if (on[v]) put(dh_out + c[v], f);
   }
-  __device__ __forceinline__ void put_dy(int v, const float (&f)[8]) const {
-    if (on[v]) st_vec8<T>(dy_out + c[v], f);
+  __device__ __forceinline__ void put_dy(int v, const uint64_t (&f)[4]) const {
+    if (on[v]) put(dy_out + c[v], f);
+  }
+  __device__ __forceinline__ static void put(T* at, const uint64_t (&f)[4]) {
+    float x[8];
+    lanes8(f, x);
+    st_vec8<T>(at, x);
   }
   __device__ __forceinline__ void end() {
     if (dh_out) dh_out += p.dh.ld;
@@ -504,9 +518,8 @@ struct ElemRows {
     }
   }
   template <int WHICH>
-  __device__ __forceinline__ void get(int v, float (&f)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  __device__ __forceinline__ void get(int v, uint64_t (&pairs)[4]) const {
+    float f[8] = {};
     if (WHICH == kDh) from_matrix(p.dh_out, v, f);
     if (WHICH == kDu && p.du.data) from_matrix(p.du, v, f);
     if (WHICH == kY) {
@@ -521,13 +534,19 @@ struct ElemRows {
       else
         from_matrix(p.h_out, v, f);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pairs[i] = pair(f[2 * i], f[2 * i + 1]);
   }
   __device__ __forceinline__ bool wants_dh() const { return p.dh.data != nullptr; }
-  __device__ __forceinline__ void put_dh(int v, const float (&f)[8]) const {
-    frag_store<T, false>(p.dh, row, v, t, tpr, p.cols, f);
+  __device__ __forceinline__ void put_dh(int v, const uint64_t (&f)[4]) const {
+    float x[8];
+    lanes8(f, x);
+    frag_store<T, false>(p.dh, row, v, t, tpr, p.cols, x);
   }
-  __device__ __forceinline__ void put_dy(int v, const float (&f)[8]) const {
-    frag_store<T, false>(p.dy, row, v, t, tpr, p.cols, f);
+  __device__ __forceinline__ void put_dy(int v, const uint64_t (&f)[4]) const {
+    float x[8];
+    lanes8(f, x);
+    frag_store<T, false>(p.dy, row, v, t, tpr, p.cols, x);
   }
   __device__ __forceinline__ void end() { ++row; }
 };
@@ -606,15 +625,16 @@ __global__ void __launch_bounds__(kJoinCta, 1)
   float* post = reinterpret_cast<float*>(dyn) + t;
   float* mine = post + 8 * NV * tpr;
   Rows in(p, lo, hi, (uint32_t)__cvta_generic_to_shared(dyn) + 16 * NV * tpr * 4);
-  float wpre[NV][8], q[NV][8], acc[NV][8], e[NV][8];
+  uint64_t wpre[NV][4], q[NV][4], acc[NV][4], e[NV][4];
   stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      wpre[v][i] = mine[(v * 8 + i) * tpr];
-      acc[v][i] = e[v][i] = 0.f;
-      post[(v * 8 + i) * tpr] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int at = (v * 8 + 2 * i) * tpr;
+      wpre[v][i] = pair(mine[at], mine[at + tpr]);
+      acc[v][i] = e[v][i] = 0;
+      post[at] = post[at + tpr] = 0.f;
     }
   int64_t grow = gate_row_of(p.gate_rows, lo);
   int64_t gate_end = p.gate_rows > 0 ? min(hi, (grow + 1) * p.gate_rows) : hi;
@@ -626,14 +646,20 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[v][i] = p.branch_scale * mine[(v * 8 + i) * tpr];
+        for (int i = 0; i < 4; ++i) {
+          const int at = (v * 8 + 2 * i) * tpr;
+          q[v][i] = mul2(pair(p.branch_scale, p.branch_scale), pair(mine[at], mine[at + tpr]));
+        }
       if (p.gate.data) {
         stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, tpr, p.cols, mine,
                              tpr);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[v][i] *= mine[(v * 8 + i) * tpr];
+          for (int i = 0; i < 4; ++i) {
+            const int at = (v * 8 + 2 * i) * tpr;
+            q[v][i] = mul2(q[v][i], pair(mine[at], mine[at + tpr]));
+          }
       }
     }
     in.begin();
@@ -644,19 +670,17 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       const uint64_t rr = pair(r1, r1);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float d[8], u[8], h[8], y[8];
+        uint64_t d[4], u[4], h[4], y[4];
         in.template get<kDh>(v, d);
         in.template get<kDu>(v, u);
         in.template get<kY>(v, y);
         in.template get<kH>(v, h);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const uint64_t wu = mul2(pair(wpre[v][i], wpre[v][i + 1]), pair(u[i], u[i + 1]));
-          const uint64_t qy = mul2(pair(q[v][i], q[v][i + 1]), pair(y[i], y[i + 1]));
-          const uint64_t hh = pair(h[i], h[i + 1]);
-          s2 = fma2(wu, hh, s2);
-          a2 = fma2(qy, fma2(rr, wu, pair(d[i], d[i + 1])), a2);
-          b2 = fma2(qy, hh, b2);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t wu = mul2(wpre[v][i], u[i]), qy = mul2(q[v][i], y[i]);
+          s2 = fma2(wu, h[i], s2);
+          a2 = fma2(qy, fma2(rr, wu, d[i]), a2);
+          b2 = fma2(qy, h[i], b2);
         }
       }
       sum[0] = lane0(s2) + lane1(s2);
@@ -671,35 +695,24 @@ __global__ void __launch_bounds__(kJoinCta, 1)
                      k2p = pair(-k2, -k2);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float d[8], u[8], h[8], y[8];
+        uint64_t d[4], u[4], h[4], y[4];
         in.template get<kDh>(v, d);
         in.template get<kDu>(v, u);
         in.template get<kY>(v, y);
         in.template get<kH>(v, h);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const uint64_t u2 = pair(u[i], u[i + 1]), y2 = pair(y[i], y[i + 1]);
-          const uint64_t h2 = pair(h[i], h[i + 1]);
-          const uint64_t full =
-              fma2(k1p, h2, fma2(r1p, mul2(pair(wpre[v][i], wpre[v][i + 1]), u2),
-                                 pair(d[i], d[i + 1])));
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t full = fma2(k1p, h[i], fma2(r1p, mul2(wpre[v][i], u[i]), d[i]));
           const uint64_t fr = mul2(full, r2p);
-          const uint64_t ac = fma2(u2, mul2(h2, r1p), pair(acc[v][i], acc[v][i + 1]));
-          const uint64_t ee = fma2(fr, y2, pair(e[v][i], e[v][i + 1]));
-          const uint64_t dy = fma2(k2p, y2, mul2(pair(q[v][i], q[v][i + 1]), fr));
-          acc[v][i] = lane0(ac);
-          acc[v][i + 1] = lane1(ac);
-          e[v][i] = lane0(ee);
-          e[v][i + 1] = lane1(ee);
-          d[i] = lane0(full);
-          d[i + 1] = lane1(full);
-          u[i] = lane0(dy);
-          u[i + 1] = lane1(dy);
+          acc[v][i] = fma2(u[i], mul2(h[i], r1p), acc[v][i]);
+          e[v][i] = fma2(fr, y[i], e[v][i]);
+          u[i] = fma2(k2p, y[i], mul2(q[v][i], fr));  // dy
+          d[i] = full;
         }
         if (in.wants_dh()) {
           if (p.res_scale != 1.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] *= p.res_scale;
+            for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], pair(p.res_scale, p.res_scale));
           }
           in.put_dh(v, d);
         }
@@ -711,9 +724,11 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mine[(v * 8 + i) * tpr] = p.branch_scale * e[v][i];
-          e[v][i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int at = (v * 8 + 2 * i) * tpr;
+          mine[at] = p.branch_scale * lane0(e[v][i]);
+          mine[at + tpr] = p.branch_scale * lane1(e[v][i]);
+          e[v][i] = 0;
         }
       close_gate_row<VEC, NV>(p, blockIdx.x, lo, hi, row, first_gate, t, post, mine, tpr);
       first_gate = false;
@@ -728,7 +743,8 @@ __global__ void __launch_bounds__(kJoinCta, 1)
     for (int i = 0; i < 8; ++i) {
       const int c = column<VEC>(v, i, t, tpr);
       if (c >= p.cols) continue;
-      if (p.dw_pre) part_row(p, blockIdx.x, kPartWPre)[c] = acc[v][i];
+      if (p.dw_pre)
+        part_row(p, blockIdx.x, kPartWPre)[c] = i & 1 ? lane1(acc[v][i / 2]) : lane0(acc[v][i / 2]);
       if (p.dw_post) part_row(p, blockIdx.x, kPartWPost)[c] = post[(v * 8 + i) * tpr];
     }
 }

@@ -51,6 +51,30 @@ __device__ __forceinline__ void st_any(void* p, int dtype, int64_t i, float x) {
     static_cast<float*>(p)[i] = x;
 }
 
+// Two fp32 lanes in one instruction (sm_100 and later).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float lane0(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float lane1(uint64_t x) {
+  return __uint_as_float((uint32_t)(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Eight consecutive elements at a 16-byte aligned address.
 __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, bf16) {
   a = __uint_as_float(w << 16);
@@ -109,6 +133,15 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&f)[8]) {
   }
 }
 
+// The same as four pairs of lanes.
+template <class T>
+__device__ __forceinline__ void widen_pairs(const Raw8<T>& r, uint64_t (&f)[4]) {
+  float x[8];
+  widen8<T>(r, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+
 template <class T>
 __device__ __forceinline__ void st_vec8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
@@ -118,30 +151,6 @@ __device__ __forceinline__ void st_vec8(T* p, const float (&f)[8]) {
     st_stream16u(p, pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
                  pack2(f[6], f[7], T()));
   }
-}
-
-// Two fp32 lanes in one instruction (sm_100 and later).
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ float lane0(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float lane1(uint64_t x) {
-  return __uint_as_float((uint32_t)(x >> 32));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -247,21 +256,29 @@ __device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int c
   if ((threadIdx.x & 3) == 0) o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
 }
 
-// Eight codes (two words) times a scale.  A code with its sign bit turned over is
-// code + 128; placed in the low byte of 2^23 it is the float 2^23 + 128 + code.
-// No integer-to-float conversions, which run at a fraction of the rate.
-__device__ __forceinline__ void act8_values(uint2 c, float scale, float (&f)[8]) {
+// Eight codes (two words) times a scale, as four pairs.  A code with its sign bit
+// turned over is code + 128; placed in the low byte of 2^23 it is the float 2^23 +
+// 128 + code.  No integer-to-float conversions, which run at a fraction of the
+// rate.
+__device__ __forceinline__ void act8_pairs(uint2 c, float scale, uint64_t (&f)[4]) {
   const uint64_t s2 = pair(scale, scale), off = pair(-8388736.f, -8388736.f);
   c.x ^= 0x80808080u;
   c.y ^= 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint32_t w = i < 4 ? c.x : c.y;
-    const uint64_t v = pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + (i & 3))),
-                            __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7541 + (i & 3))));
-    const uint64_t r = mul2(add2(v, off), s2);
-    f[i] = lane0(r);
-    f[i + 1] = lane1(r);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? c.x : c.y;
+    const uint64_t v = pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + 2 * (i & 1))),
+                            __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7541 + 2 * (i & 1))));
+    f[i] = mul2(add2(v, off), s2);
+  }
+}
+__device__ __forceinline__ void act8_values(uint2 c, float scale, float (&f)[8]) {
+  uint64_t q[4];
+  act8_pairs(c, scale, q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = lane0(q[i]);
+    f[2 * i + 1] = lane1(q[i]);
   }
 }
 

@@ -31,13 +31,15 @@ _NO_ACT8 = (0, 0, 0, 0)
 
 _torch = None
 _types: dict = {}
+_raw_stream = None
 
 
 def _load():
     """torch, imported at the first call, and the dtype codes."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _types.update({torch.bfloat16: DPOPT_GRAD_BF16, torch.float16: DPOPT_GRAD_F16,
                        torch.float32: DPOPT_GRAD_F32})
         _torch = torch
@@ -53,6 +55,8 @@ def _dtype(t, name: str) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:  # the same handle without the stream object's 3 us
+            return _raw_stream(_torch.cuda.current_device())
         return _torch.cuda.current_stream().cuda_stream
     return int(getattr(stream, "cuda_stream", stream))
 
