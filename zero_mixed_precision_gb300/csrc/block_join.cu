@@ -9,15 +9,16 @@
 namespace dpopt {
 namespace {
 
-// A row is held by one CTA of tpr threads (a multiple of 32), 16 columns a thread
-// (32 beyond 8192 columns) as fragments of 8.  In the vector form (every matrix
-// may be moved 16 bytes at a time, up to 8192 columns) thread t's fragment v is the
-// columns (v tpr + t) 8 .. + 7; in the element form its element i is column
+// A row is held by one CTA of tpr threads (a multiple of 32), NV fragments of 8
+// columns a thread: one (two beyond 8192 columns) in CTAs of up to 1024 threads
+// of 64 registers, or two in CTAs of up to 512 threads of 128 where a thread
+// keeps sums over rows as well.  In the vector form (every matrix may be moved 16
+// bytes at a time, up to 8192 columns) thread t's fragment v is the columns
+// (v tpr + t) 8 .. + 7; in the element form its element i is column
 // (v 8 + i) tpr + t, so that a warp always touches neighbouring columns.  Either
 // way a block of 32 columns lies in one warp.  The row index depends on blockIdx
 // alone, which keeps row addresses out of the threads' registers.
-constexpr int kJoinCta = 512, kJoinSms = 152, kVecFrags = 2;
-constexpr int kVecCols = kJoinCta * 8 * kVecFrags;
+constexpr int kJoinSms = 152, kVecCols = 8192;
 
 struct JoinParams {
   int64_t rows;
@@ -31,16 +32,14 @@ struct JoinParams {
   Dbg dbg;
 };
 
-__host__ __device__ inline int row_frags(int64_t cols) { return cols <= kVecCols ? 2 : 4; }
-__host__ __device__ inline int row_threads(int64_t cols) {
-  const int64_t per_warp = 256 * row_frags(cols);
-  return (int)((cols + per_warp - 1) / per_warp) * 32;
+__host__ __device__ inline int row_threads(int64_t cols, int nv) {
+  return (int)((cols + 256 * nv - 1) / (256 * nv)) * 32;
 }
 
 // Sum of N values over a CTA, the same bits in each thread: the warps'
 // butterflies, then the warps' sums in warp order (or as a butterfly).  Callers
 // alternate between two slot arrays, so that one barrier is enough.
-template <int N>
+template <int N, int MAXT>
 __device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
@@ -56,10 +55,10 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr
       x[i] = slot[0][i];
       for (int w = 1; w < warps; ++w) x[i] += slot[w][i];
     } else {
-      const int w = lane & (kJoinCta / 32 - 1);  // both halves of the warp alike
+      const int w = lane & (MAXT / 32 - 1);  // with 16 warps both halves alike
       x[i] = w < warps ? slot[w][i] : 0.f;
 #pragma unroll
-      for (int o = kJoinCta / 64; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+      for (int o = MAXT / 64; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
     }
   }
 }
@@ -105,11 +104,13 @@ __host__ __device__ inline int64_t gate_row_of(int64_t gate_rows, int64_t row) {
 // A CTA walks rows; the next row's h and y are loaded before the present row's
 // two sums, and h_out stays in registers in fp32 between the norms.  The
 // parameters are kept as branch_scale * gate * w_post and w_pre.
+constexpr int kRowCta = 1024;
+
 template <class T, bool VEC, int NV>
-__global__ void __launch_bounds__(kJoinCta, 1)
+__global__ void __launch_bounds__(kRowCta, 1)
     block_join_kernel(const __grid_constant__ JoinParams p) {
   pdl_enter();
-  __shared__ float slot[2][kJoinCta / 32][1];
+  __shared__ float slot[2][kRowCta / 32][1];
   extern __shared__ float stage[];  // 8 NV places per thread
   const int t = threadIdx.x, tpr = blockDim.x;
   const int cols = p.cols;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[v][i], y[v][i], ss[0]);
-      row_sum<1>(ss, slot[0], tpr);
+      row_sum<1, kRowCta>(ss, slot[0], tpr);
       rpost = rsqrtf(fmaf(ss[0], inv_c, p.eps));
       if (t == 0) p.rstd_post[row] = rpost;
     }
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       __syncthreads();  // the only sum's slots are used again in the next row
       continue;
     }
-    row_sum<1>(ss, slot[1], tpr);
+    row_sum<1, kRowCta>(ss, slot[1], tpr);
     const float rpre = rsqrtf(fmaf(ss[0], inv_c, p.eps));
     if (t == 0) p.rstd_pre[row] = rpre;
 #pragma unroll
@@ -216,12 +217,11 @@ __global__ void __launch_bounds__(kJoinCta, 1)
 // the sizes alone (as many as 152 SMs hold CTAs at a time, but no run of fewer
 // than kPartMinRows rows when there are more rows than SMs).  Each run's CTA leaves one partial row per sum in scratch and the finish kernel adds them
 // in order, so the result does not depend on the GPU or on timing.
-constexpr int kPartMinRows = 4;
+constexpr int kPartMinRows = 4, kGradCta = 512, kGradFrags = 2;
 
-// CTAs of the gradient's kernel an SM holds (its registers are sized for kJoinCta
-// threads).
+// CTAs of the gradient's kernel an SM holds.
 __host__ __device__ inline int ctas_per_sm(int64_t cols) {
-  const int n = kJoinCta / row_threads(cols);
+  const int n = kGradCta / row_threads(cols, kGradFrags);
   return n < 1 ? 1 : n;
 }
 __host__ __device__ inline int64_t part_rows(int64_t rows, int64_t cols) {
@@ -306,7 +306,7 @@ __device__ __forceinline__ void lanes8(const uint64_t (&f)[4], float (&x)[8]) {
 // zeros throughout.
 template <class T, int YP, int HP>
 struct VecRows {
-  static constexpr int NV = kVecFrags;
+  static constexpr int NV = kGradFrags, kMaxThreads = kGradCta;
   static constexpr uint32_t kWide = 8 * sizeof(T), kNarrow = 8;
   static constexpr uint32_t kYBytes = YP ? kNarrow : kWide, kHBytes = HP == 2 ? kNarrow : kWide;
   const JoinGradParams& p;
@@ -488,7 +488,7 @@ struct VecRows {
 // Element form: straight from global memory, the second reading of a row from L1.
 template <class T, int NV_>
 struct ElemRows {
-  static constexpr int NV = NV_;
+  static constexpr int NV = NV_, kMaxThreads = kRowCta;
   const JoinGradParams& p;
   const int t, tpr;
   int64_t row;
@@ -610,12 +610,12 @@ __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t par
 // the gate row stays the same, dw_post grows by branch gate e and dgate is branch
 // w_post e.
 template <class T, bool VEC, class Rows>
-__global__ void __launch_bounds__(kJoinCta, 1)
+__global__ void __launch_bounds__(Rows::kMaxThreads, 1)
     block_join_grad_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   constexpr int NV = Rows::NV;
   extern __shared__ __align__(16) unsigned char dyn[];
-  __shared__ float slot[2][kJoinCta / 32][3];
+  __shared__ float slot[2][Rows::kMaxThreads / 32][3];
   const int t = threadIdx.x, tpr = blockDim.x;
   const int64_t lo = blockIdx.x * p.per, hi = min(p.rows, lo + p.per);
   if (!dbg_ok(p.dbg, tpr * 8 * NV >= p.cols && lo < hi)) return;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kJoinCta, 1)
       sum[1] = lane0(a2) + lane1(a2);
       sum[2] = lane0(b2) + lane1(b2);
     }
-    row_sum<3>(sum, slot[row & 1], tpr);
+    row_sum<3, Rows::kMaxThreads>(sum, slot[row & 1], tpr);
     const float k1 = r1 * r1 * r1 * sum[0] * inv_c;
     const float k2 = p.rstd_post ? r2 * r2 * r2 * (sum[1] - k1 * sum[2]) * inv_c : 0.f;
     {
@@ -844,12 +844,13 @@ constexpr size_t kJoinSmem = 220 * 1024;  // of 227 KB; the static arrays need s
 template <class T, bool VEC, int NV>
 int launch_join_at(JoinParams& p, cudaStream_t stream) {
   constexpr auto kern = block_join_kernel<T, VEC, NV>;
+  p.tpr = row_threads(p.cols, NV);
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const size_t smem = (size_t)p.tpr * 8 * NV * sizeof(float);
   DPOPT_TRY(allow_smem<kern>(smem));
   // CTAs an SM holds, asked once per CTA size
-  static std::atomic<int> resident[kJoinCta / 32 + 1];
+  static std::atomic<int> resident[kRowCta / 32 + 1];
   std::atomic<int>& held = resident[p.tpr / 32];
   int per_sm = held.load(std::memory_order_relaxed);
   if (per_sm == 0) {
@@ -865,38 +866,44 @@ int launch_join_at(JoinParams& p, cudaStream_t stream) {
 
 template <class T>
 int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
-  if (vec) return launch_join_at<T, true, kVecFrags>(p, stream);
-  return row_frags(p.cols) == 2 ? launch_join_at<T, false, 2>(p, stream)
-                                : launch_join_at<T, false, 4>(p, stream);
+  if (vec) return launch_join_at<T, true, 1>(p, stream);
+  return p.cols <= 8 * kRowCta ? launch_join_at<T, false, 1>(p, stream)
+                               : launch_join_at<T, false, 2>(p, stream);
 }
 
 template <class T, bool VEC, class Rows>
-int launch_grad_at(JoinGradParams& p, size_t room, cudaStream_t stream) {
+int launch_grad_at(JoinGradParams& p, size_t smem, cudaStream_t stream) {
   constexpr auto kern = block_join_grad_kernel<T, VEC, Rows>;
-  const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
-  p.stages = VEC ? (int)std::min<size_t>(3, (room - sums) / p.stage_bytes) : 0;
-  const size_t smem = sums + (size_t)p.stages * p.stage_bytes;
   DPOPT_TRY(allow_smem<kern>(smem));
   return launched(launch_pdl(kern, (unsigned)p.parts, p.tpr, smem, stream, p),
                   "block join gradient");
 }
 
+template <class T>
+int launch_grad_elem(JoinGradParams& p, cudaStream_t stream) {
+  const int nv = p.cols <= 8 * kRowCta ? 1 : 2;
+  p.tpr = row_threads(p.cols, nv);
+  const size_t sums = (size_t)p.tpr * 16 * nv * sizeof(float);
+  return nv == 1 ? launch_grad_at<T, false, ElemRows<T, 1>>(p, sums, stream)
+                 : launch_grad_at<T, false, ElemRows<T, 2>>(p, sums, stream);
+}
+
 template <class T, int YP, int HP>
 int launch_grad_vec(JoinGradParams& p, cudaStream_t stream) {
   using Rows = VecRows<T, YP, HP>;
+  p.tpr = row_threads(p.cols, Rows::NV);
   const size_t room = kJoinSmem / ctas_per_sm(p.cols);
   const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
   p.stage_bytes = Rows::stage_bytes(p.tpr);
   // the ring needs room for at least one row
-  if (sums + p.stage_bytes > room) return launch_grad_at<T, false, ElemRows<T, 2>>(p, room, stream);
-  return launch_grad_at<T, true, Rows>(p, room, stream);
+  if (sums + p.stage_bytes > room) return launch_grad_elem<T>(p, stream);
+  p.stages = (int)std::min<size_t>(3, (room - sums) / p.stage_bytes);
+  return launch_grad_at<T, true, Rows>(p, sums + p.stages * (size_t)p.stage_bytes, stream);
 }
 
 template <class T>
 int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
-  if (!vec)
-    return row_frags(p.cols) == 2 ? launch_grad_at<T, false, ElemRows<T, 2>>(p, 0, stream)
-                                  : launch_grad_at<T, false, ElemRows<T, 4>>(p, 0, stream);
+  if (!vec) return launch_grad_elem<T>(p, stream);
   if (!p.du.data)
     return p.y8.codes ? launch_grad_vec<T, 1, 0>(p, stream) : launch_grad_vec<T, 0, 0>(p, stream);
   if (p.h8.codes)
@@ -952,7 +959,6 @@ int dpopt_block_join(const dpopt_block_join_args* a, dpopt_stream_t stream) {
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
   p.cols = (int)cols;
-  p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.eps = a->eps;
   p.res_scale = a->res_scale;
@@ -1050,7 +1056,6 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   DPOPT_TRY(check_overlaps(s, n));
   p.rows = rows;
   p.cols = (int)cols;
-  p.tpr = row_threads(cols);
   p.param_dtype = a->param_dtype;
   p.res_scale = a->res_scale;
   p.branch_scale = a->branch_scale;
