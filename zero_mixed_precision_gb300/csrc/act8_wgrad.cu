@@ -93,7 +93,13 @@ __global__ void __launch_bounds__(kOperandThreads)
 // CTA copies 32 KB, for four times the products of a 128 x 128 tile's 32 KB.
 constexpr int kTileM = 128, kStep = 64;
 constexpr int kBoxBytes = 64 * kStep * 2;  // one copied box: 64 columns x kStep tokens
-constexpr int kGemmThreads = 192;          // copying warp, issuing warp, four epilogue warps
+// The tensor cores cut off where an fp32 addition would round, which over a long
+// sum drifts (1.4e-6 of the result over 2011 tokens, against 3e-7 for additions
+// that round).  Results in fp32 are therefore summed over kShortSteps steps (512
+// tokens) at a time in tensor memory, and those sums in registers, by eight
+// epilogue warps in place of four; for 16-bit results the drift is far below
+// their rounding.
+constexpr int kShortSteps = 8;
 constexpr int kTileGroup = 16;             // row tiles that run side by side (shared columns in L2)
 
 struct GemmParams {
@@ -108,8 +114,12 @@ struct GemmParams {
   Dbg dbg;
 };
 
-template <int CG, int BN>
+template <int CG, int BN, bool SHORT>
 struct GemmShape {
+  // a copying warp, an issuing warp, and the epilogue's: four tensor-memory
+  // quarters by one or two halves of the columns
+  static constexpr int kHalves = SHORT ? 2 : 1, kThreads = 64 + 128 * kHalves;
+  static constexpr int kCols = BN / kHalves;  // of an epilogue warp
   static constexpr int kBoxesA = kTileM / 64, kBoxesB = BN / CG / 64;
   static constexpr int kStageBytes = (kBoxesA + kBoxesB) * kBoxBytes;
   static constexpr int kStages = 6;
@@ -251,6 +261,17 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // Unit u of a launch: the tile's corner and the range of token steps.
 struct Unit {
   int m0, n0, split, steps;
@@ -275,28 +296,77 @@ __device__ __forceinline__ Unit unit_at(const GemmParams& p, int u) {
   return r;
 }
 
-// Rows row0 .. + rows of column c, the sums at x[33 i]: the addend's values are all
-// asked for before the first store.
-template <class T>
+// Rows row0 .. + rows of column c, the sums at x[33 i]: 16 of the addend's values
+// are asked for before the first store.
+template <class T, bool ADD>
 __device__ __forceinline__ void store_columns(const GemmParams& p, int row0, int c, int rows,
                                               const float* x) {
-  T add[32];
-  if (p.addend.data) {
-    const T* a = static_cast<const T*>(p.addend.data) + row0 * p.addend.ld + c;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) add[i] = i < rows ? a[i * p.addend.ld] : from_f32<T>(0.f);
-  }
+  constexpr int kBatch = 16;
+  const T* a = ADD && p.addend.data
+                   ? static_cast<const T*>(p.addend.data) + row0 * p.addend.ld + c
+                   : nullptr;
   T* d = static_cast<T*>(p.dw.data) + row0 * p.dw.ld + c;
+  for (int i0 = 0; i0 < rows; i0 += kBatch) {
+    T add[kBatch];
+    if (a)
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < rows)
-      d[i * p.dw.ld] = from_f32<T>(p.addend.data ? x[33 * i] + to_f32(add[i]) : x[33 * i]);
+      for (int i = 0; i < kBatch; ++i)
+        if (i0 + i < rows) add[i] = a[(i0 + i) * p.addend.ld];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i0 + i < rows) {
+        const float s = x[33 * (i0 + i)];
+        d[(i0 + i) * p.dw.ld] = from_f32<T>(a ? s + to_f32(add[i]) : s);
+      }
+  }
+}
+
+// N columns, row row0 + lane, of an fp32 addend; zeros without one or out of range.
+// Aligned rows are read by their lanes in vectors, others by the warp a row at a
+// time and turned in shared memory.
+template <int N>
+__device__ __forceinline__ void load_addend(const GemmParams& p, int row0, int col, float (&f)[N],
+                                            float* swap) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = 0.f;
+  if (!p.addend.data || p.splits > 1) return;
+  const int lane = threadIdx.x & 31;
+  const float* a = static_cast<const float*>(p.addend.data);
+  if (p.addend.vec && col + N <= p.k) {
+    if (row0 + lane >= p.n) return;
+    a += (row0 + lane) * p.addend.ld + col;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(a + i);
+      f[i] = x.x;
+      f[i + 1] = x.y;
+      f[i + 2] = x.z;
+      f[i + 3] = x.w;
+    }
+    return;
+  }
+  a += row0 * p.addend.ld + col + lane;
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      x[i] = row0 + i < p.n && col + c + lane < p.k ? a[i * p.addend.ld + c] : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) swap[i * 33 + lane] = x[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[c + i] = swap[lane * 33 + i];
+  }
 }
 
 // 32 rows x 32 columns of a tile, a row per lane, from a warp's registers to memory.
 // Partial sums, and results without an addend whose rows are 16-byte aligned, go
 // out as vectors, a row's 32 columns per lane; others go through shared memory
 // (`swap`, 32 x 33) so that a warp's loads and stores touch neighbouring columns.
+// ADD: the addend is still to be added.
+template <bool ADD>
 __device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int row0, int col,
                                         const uint32_t (&r)[32], float* swap) {
   const int lane = threadIdx.x & 31, row = row0 + lane;
@@ -309,7 +379,7 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int 
         *reinterpret_cast<uint4*>(dst + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
     return;
   }
-  if (p.dw.vec && !p.addend.data && col + 32 <= p.k) {
+  if (p.dw.vec && !(ADD && p.addend.data) && col + 32 <= p.k) {
     if (row >= p.n) return;
     const int64_t at = row * p.dw.ld + col;
     if (p.out_dtype == DPOPT_GRAD_F32) {
@@ -341,31 +411,31 @@ __device__ __forceinline__ void store32(const GemmParams& p, const Unit& u, int 
   const int c = col + lane, rows = min(32, p.n - row0);
   if (c >= p.k || rows <= 0) return;
   if (p.out_dtype == DPOPT_GRAD_F32)
-    store_columns<float>(p, row0, c, rows, swap + lane);
+    store_columns<float, ADD>(p, row0, c, rows, swap + lane);
   else if (p.out_dtype == DPOPT_GRAD_BF16)
-    store_columns<bf16>(p, row0, c, rows, swap + lane);
+    store_columns<bf16, ADD>(p, row0, c, rows, swap + lane);
   else
-    store_columns<fp16>(p, row0, c, rows, swap + lane);
+    store_columns<fp16, ADD>(p, row0, c, rows, swap + lane);
 }
 
 // One warp copies boxes into a ring of stages, one (of a pair's first CTA) issues
-// the products of a stage (four of 16 tokens), four bring finished tiles from
-// tensor memory to memory; two accumulators let the next tile's products run
-// under a tile's epilogue.  In a pair the first CTA's `full` counts both CTAs'
+// the products of a stage (four of 16 tokens), four or eight bring finished sums
+// from tensor memory to memory; two accumulators let the next sum's products run
+// under a sum's epilogue.  In a pair the first CTA's `full` counts both CTAs'
 // bytes and its `taken` both CTAs' epilogue warps; `empty` and `done` are arrived
 // on in both.
-template <class T, int CG, int BN>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <class T, int CG, int BN, bool SHORT>
+__global__ void __launch_bounds__((GemmShape<CG, BN, SHORT>::kThreads), 1)
     act8_wgrad_kernel(const __grid_constant__ GemmParams p,
                       const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b) {
-  using S = GemmShape<CG, BN>;
+  using S = GemmShape<CG, BN, SHORT>;
   extern __shared__ unsigned char dyn[];
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], done[2], taken[2],
       drained;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort;
-  __shared__ float swap[4][32 * 33];
+  __shared__ float swap[4 * S::kHalves][32 * 33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : blockIdx.x & 1;
   const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
@@ -376,7 +446,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&done[a]), 1);
-      mbar_init(smem_u32(&taken[a]), 4 * CG);
+      mbar_init(smem_u32(&taken[a]), 4 * S::kHalves * CG);
     }
     mbar_init(smem_u32(&drained), 1);
     abort = 0;
@@ -440,27 +510,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int64_t it = 0;
       int count = 0;
       bool ok = true;
-      for (int u = first; ok && u < units; u += stride, ++count) {
+      for (int u = first; ok && u < units; u += stride) {
         const Unit q = unit_at<CG, BN>(p, u);
-        const int a = count & 1;
-        if (!(ok = gemm_wait(smem_u32(&taken[a]), ((count >> 1) & 1) ^ 1, p.wait_limit, &abort)))
-          break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + a * BN;
-        for (int step = 0; step < q.steps; ++step, ++it) {
-          const int s = (int)(it % S::kStages);
-          const uint32_t round = (uint32_t)(it / S::kStages);
-          if (!(ok = gemm_wait(smem_u32(&full[s]), round & 1, p.wait_limit, &abort))) break;
+        int step = 0;
+        while (ok && step < q.steps) {  // one accumulator's sum
+          const int a = count & 1, end = SHORT ? min(q.steps, step + kShortSteps) : q.steps;
+          if (!(ok = gemm_wait(smem_u32(&taken[a]), ((count >> 1) & 1) ^ 1, p.wait_limit, &abort)))
+            break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t at = ring + s * S::kStageBytes;
-          const uint64_t da = operand_desc(at);
-          const uint64_t db = operand_desc(at + S::kBoxesA * kBoxBytes);
+          const uint32_t d = tmem + a * BN;
+          for (bool add = false; step < end; ++step, ++it) {
+            const int s = (int)(it % S::kStages);
+            const uint32_t round = (uint32_t)(it / S::kStages);
+            if (!(ok = gemm_wait(smem_u32(&full[s]), round & 1, p.wait_limit, &abort))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t at = ring + s * S::kStageBytes;
+            const uint64_t da = operand_desc(at);
+            const uint64_t db = operand_desc(at + S::kBoxesA * kBoxBytes);
 #pragma unroll
-          for (int j = 0; j < kStep / 16; ++j)  // 16 tokens are 2048 bytes further on
-            mma_16<CG>(d, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc, step > 0 || j > 0);
-          mma_commit<CG>(smem_u32(&empty[s]));
+            for (int j = 0; j < kStep / 16; ++j) {  // 16 tokens are 2048 bytes further on
+              mma_16<CG>(d, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc, add);
+              add = true;
+            }
+            mma_commit<CG>(smem_u32(&empty[s]));
+          }
+          if (ok) mma_commit<CG>(smem_u32(&done[a]));
+          ++count;
         }
-        if (ok) mma_commit<CG>(smem_u32(&done[a]));
       }
       if (!ok) {
         // products in flight end before tensor memory is given back
@@ -473,28 +549,61 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
   } else {
     const int quarter = warp & 3;  // the tensor-memory lanes this warp may read
-    int count = 0;
-    for (int u = first; u < units; u += stride, ++count) {
-      const Unit q = unit_at<CG, BN>(p, u);
-      const int a = count & 1;
-      const bool ok = gemm_wait(smem_u32(&done[a]), (count >> 1) & 1, p.wait_limit, &abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
+    const int col0 = SHORT ? (warp - 2) / 4 * S::kCols : 0;
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21) + col0;
+    auto await = [&](int count) {
+      const bool ok = gemm_wait(smem_u32(&done[count & 1]), (count >> 1) & 1, p.wait_limit, &abort);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int row0 = q.m0 + rank * kTileM + quarter * 32;
-      for (int c = 0; c < BN && q.n0 + c < p.k; c += 32) {
-        uint32_t r[32];
-        tmem_load32(tmem + ((uint32_t)quarter << 21) + a * BN + c, r);
-        store32(p, q, row0, q.n0 + c, r, swap[quarter]);
-      }
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto release = [&](int count) {
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 1)
-          mbar_arrive(smem_u32(&taken[a]));
-        else
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                           in_cta(smem_u32(&taken[a]), 0))
-                       : "memory");
+      if (lane != 0) return;
+      if constexpr (CG == 1)
+        mbar_arrive(smem_u32(&taken[count & 1]));
+      else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         in_cta(smem_u32(&taken[count & 1]), 0))
+                     : "memory");
+    };
+    int count = 0;
+    bool ok = true;
+    for (int u = first; ok && u < units; u += stride) {
+      const Unit q = unit_at<CG, BN>(p, u);
+      const int row0 = q.m0 + rank * kTileM + quarter * 32, n0 = q.n0 + col0;
+      if constexpr (SHORT) {
+        // the sums start from the addend, which is read while the products run
+        float sum[S::kCols];
+        load_addend<S::kCols>(p, row0, n0, sum, swap[warp - 2]);
+        for (int step = 0; step < q.steps; step += kShortSteps, ++count) {
+          if (!(ok = await(count))) break;
+#pragma unroll
+          for (int c = 0; c < S::kCols; c += 16) {  // 16 at a time: the sums fill the registers
+            uint32_t r[16];
+            tmem_load16(lanes + (count & 1) * BN + c, r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              sum[c + i] += __uint_as_float(r[i]);
+          }
+          release(count);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < S::kCols; c += 32) {
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[c + i]);
+          if (n0 + c < p.k) store32<false>(p, q, row0, n0 + c, r, swap[warp - 2]);
+        }
+      } else {
+        if (!(ok = await(count))) break;
+        for (int c = 0; c < S::kCols && n0 + c < p.k; c += 32) {
+          uint32_t r[32];
+          tmem_load32(lanes + (count & 1) * BN + c, r);
+          store32<true>(p, q, row0, n0 + c, r, swap[warp - 2]);
+        }
+        release(count++);
       }
     }
   }
@@ -626,18 +735,18 @@ int encode(CUtensorMap* map, bool is_bf16, const void* base, int64_t cols, int64
   return DPOPT_OK;
 }
 
-template <class T, int CG, int BN>
+template <class T, int CG, int BN, bool SHORT>
 int launch_gemm(const GemmParams& p, const CUtensorMap& a, const CUtensorMap& b,
                 cudaStream_t stream) {
-  constexpr auto kern = act8_wgrad_kernel<T, CG, BN>;
-  const size_t smem = GemmShape<CG, BN>::kSmem;
+  constexpr auto kern = act8_wgrad_kernel<T, CG, BN, SHORT>;
+  const size_t smem = GemmShape<CG, BN, SHORT>::kSmem;
   DPOPT_TRY(allow_smem<kern>(smem));
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, sms / CG) * CG));
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(GemmShape<CG, BN, SHORT>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -674,8 +783,11 @@ int run_wgrad(const Plan& plan, GemmParams& g, OperandParams& o, unsigned char* 
   DPOPT_TRY(launched(
       launch_pdl(act8_operands_kernel<T>, ctas, kOperandThreads, 0, stream, o),
       "act8 weight gradient operands"));
-  return plan.pair ? launch_gemm<T, 2, 256>(g, a, b, stream)
-                   : launch_gemm<T, 1, 128>(g, a, b, stream);
+  if (g.out_dtype == DPOPT_GRAD_F32)
+    return plan.pair ? launch_gemm<T, 2, 256, true>(g, a, b, stream)
+                     : launch_gemm<T, 1, 128, true>(g, a, b, stream);
+  return plan.pair ? launch_gemm<T, 2, 256, false>(g, a, b, stream)
+                   : launch_gemm<T, 1, 128, false>(g, a, b, stream);
 }
 
 }  // namespace
