@@ -648,7 +648,9 @@ int dpopt_act8_unpack(const int8_t *codes, int64_t ld_codes, const uint8_t *exps
 
 /* Weight gradient of a linear layer y = x W^T from the packed x:
  *   dw[i][j] = sum_t dy[t][i] * value(t, j)  (+ addend[i][j]),   i < n, j < k
- *  dy              tokens x n, bf16 or fp16 (dtype; fp32: DPOPT_ERR_UNSUPPORTED).
+ *  dy              tokens x n, bf16 or fp16 (dtype; fp32: DPOPT_ERR_UNSUPPORTED), in
+ *                  device memory (not page-locked host memory: it is read by
+ *                  tensor copies).
  *  codes, exps     the packed x, tokens x k; x was of type `dtype`, so that its
  *                  values are exact operands of the products.
  *  dw              n x k of out_dtype, written.
@@ -657,7 +659,11 @@ int dpopt_act8_unpack(const int8_t *codes, int64_t ld_codes, const uint8_t *exps
  *                  same stride.
  *  scratch         DEVICE, 256-byte aligned, dpopt_act8_wgrad_scratch_bytes()
  *                  bytes, overlapping no other array.
- * Products are summed in fp32.  tokens = 0 writes the addend, or zeros.
+ * Products are exact and summed in fp32: over the whole of a split of the tokens on
+ * the tensor cores for 16-bit results; for fp32 results 512 tokens at a time there
+ * and those sums by rounded fp32 additions.  tokens = 0 writes the addend, or
+ * zeros.  The kernel's waits are bounded; one that gave up is reported by
+ * dpopt_stream_status as DPOPT_ERR_TIMEOUT.
  * Errors: as above, DPOPT_ERR_INVALID_ARG for too small a scratch, and
  * DPOPT_ERR_UNSUPPORTED for a size of 2^31 or more. */
 int dpopt_act8_wgrad(const void *dy, int dtype, int64_t ld_dy, const int8_t *codes,

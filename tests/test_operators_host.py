@@ -121,6 +121,8 @@ def test_pack_refuses(dp, over, code):
     (dict(addend=A[4] + 1), 1), (dict(addend=A[4], ld_addend=3), 1),
     (dict(addend=A[3] + 4, ld_addend=96), 1), (dict(dw=A[0]), 1), (dict(dw=A[1]), 1),
     (dict(tokens=1 << 31), 2),
+    (dict(tokens=(1 << 31) - 1, k=(1 << 31) - 1, ld_codes=(1 << 31) - 1, ld_exps=1 << 26,
+          ld_dw=(1 << 31) - 1), 2),
 ])
 def test_wgrad_refuses(dp, over, code):
     a = dict(dy=A[0], dtype=0, ld_dy=64, codes=A[1], ld_codes=96, exps=A[2], ld_exps=3, tokens=70,
@@ -236,6 +238,8 @@ def test_wrappers_refuse_wrong_shapes_types_and_memory(dp):
     codes, exps = dp.act8_empty(4, 64, "cpu")
     with pytest.raises(ValueError, match="pageable"):
         dp.act8_pack(x, codes, exps, stream=0)
+    with pytest.raises(ValueError, match="device memory"):
+        dp.act8_wgrad(x, codes, exps, torch.zeros(64, 64), stream=0)
     with pytest.raises(ValueError, match="dimensions"):
         dp.act8_pack(x[0], codes, exps, stream=0)
     with pytest.raises(ValueError, match="adjacent"):

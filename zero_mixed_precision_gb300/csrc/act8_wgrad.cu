@@ -817,6 +817,10 @@ int dpopt_act8_wgrad_scratch_bytes(int64_t tokens, int64_t n, int64_t k, int64_t
   const int64_t limit = (int64_t)1 << 31;
   if (tokens >= limit || n >= limit || k >= limit)
     return fail(DPOPT_ERR_UNSUPPORTED, "sizes must be below 2^31");
+  // far beyond any memory, and safely inside 64-bit byte counts
+  if ((double)std::max(tokens, n) * (double)std::max(n, k) > 1e15 ||
+      (double)tokens * (double)k > 1e15)
+    return fail(DPOPT_ERR_UNSUPPORTED, "matrices of more than 1e15 elements");
   const Plan plan = make_plan(tokens, n, k);
   *bytes_out = plan.x_bytes + plan.dy_bytes + plan.partial_bytes;
   return DPOPT_OK;

@@ -153,6 +153,8 @@ def act8_wgrad(dy, codes, exps, dw, scratch=None, *, addend=None, stream=None) -
     _load()
     tokens, n = shape = _rows_cols(dy, "dy")
     k = _rows_cols(codes, "codes")[1]
+    if tokens and not dy.is_cuda:
+        raise ValueError("dy must be in device memory (it is read by tensor copies)")
     pdy, lddy = _matrix(dy, "dy", shape)
     c, ldc, e, lde = _packed((codes, exps), "packed", tokens, k)
     pdw, lddw = _matrix(dw, "dw", (n, k))
