@@ -551,6 +551,45 @@ struct ElemRows {
   __device__ __forceinline__ void end() { ++row; }
 };
 
+// The gradient's parameters at a thread's columns, all asked for together: w_pre
+// (where wanted) and branch_scale * w_post * gate, into the places wpre[i * stride]
+// and q[i * stride].
+template <class W, bool VEC, int NV>
+__device__ __forceinline__ void stage_typed_grad(const JoinGradParams& p, int64_t grow, int t,
+                                                 float* wpre, float* q, int stride) {
+  const W* a = static_cast<const W*>(p.w_pre);
+  const W* b = static_cast<const W*>(p.w_post);
+  const W* g = p.gate.data ? static_cast<const W*>(p.gate.data) + grow * p.gate.ld : nullptr;
+  const W one = from_f32<W>(1.f);
+  W ra[NV][8], rb[NV][8], rg[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(column<VEC>(v, i, t, p.tpr), p.cols - 1);
+      ra[v][i] = a && wpre ? a[c] : one;
+      rb[v][i] = b ? b[c] : one;
+      rg[v][i] = g ? g[c] : one;
+    }
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (wpre) wpre[(v * 8 + i) * stride] = to_f32(ra[v][i]);
+      q[(v * 8 + i) * stride] = p.branch_scale * to_f32(rb[v][i]) * to_f32(rg[v][i]);
+    }
+}
+template <bool VEC, int NV>
+__device__ __noinline__ void stage_grad(const JoinGradParams& p, int64_t grow, int t, float* wpre,
+                                        float* q, int stride) {
+  if (p.param_dtype == DPOPT_GRAD_BF16)
+    stage_typed_grad<bf16, VEC, NV>(p, grow, t, wpre, q, stride);
+  else if (p.param_dtype == DPOPT_GRAD_F16)
+    stage_typed_grad<fp16, VEC, NV>(p, grow, t, wpre, q, stride);
+  else
+    stage_typed_grad<float, VEC, NV>(p, grow, t, wpre, q, stride);
+}
+
 // At the end of a gate row's rows in a part: its sums branch_scale * e (in `mine`)
 // go into dw_post's and into dgate, or into a partial row of it.
 template <class W, bool VEC, int NV>
@@ -621,46 +660,38 @@ __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
   if (!dbg_ok(p.dbg, tpr * 8 * NV >= p.cols && lo < hi)) return;
   const float inv_c = 1.f / (float)p.cols;
   // dw_post of finished gate rows, and parameters and sums on their way: one
-  // place per column of a thread
+  // place per column of a thread.  With one gate row for all rows (gate_rows 0) a
+  // part leaves branch_scale * e itself, from which the finish kernel makes both
+  // dw_post and dgate.
   float* post = reinterpret_cast<float*>(dyn) + t;
   float* mine = post + 8 * NV * tpr;
   Rows in(p, lo, hi, (uint32_t)__cvta_generic_to_shared(dyn) + 16 * NV * tpr * 4);
   uint64_t wpre[NV][4], q[NV][4], acc[NV][4], e[NV][4];
-  stage_param<VEC, NV>(p.w_pre, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
+  int64_t grow = gate_row_of(p.gate_rows, lo);
+  int64_t gate_end = p.gate_rows > 0 ? min(hi, (grow + 1) * p.gate_rows) : INT64_MAX;
+  stage_grad<VEC, NV>(p, grow, t, post, mine, tpr);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = (v * 8 + 2 * i) * tpr;
-      wpre[v][i] = pair(mine[at], mine[at + tpr]);
+      wpre[v][i] = pair(post[at], post[at + tpr]);
+      q[v][i] = pair(mine[at], mine[at + tpr]);
       acc[v][i] = e[v][i] = 0;
       post[at] = post[at + tpr] = 0.f;
     }
-  int64_t grow = gate_row_of(p.gate_rows, lo);
-  int64_t gate_end = p.gate_rows > 0 ? min(hi, (grow + 1) * p.gate_rows) : hi;
-  bool first_gate = true, new_gate = true;
+  bool first_gate = true, new_gate = false;
   for (int64_t row = lo; row < hi; ++row) {
     if (new_gate) {
       new_gate = false;
-      stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, tpr, p.cols, mine, tpr);
+      stage_grad<VEC, NV>(p, grow, t, nullptr, mine, tpr);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at = (v * 8 + 2 * i) * tpr;
-          q[v][i] = mul2(pair(p.branch_scale, p.branch_scale), pair(mine[at], mine[at + tpr]));
+          q[v][i] = pair(mine[at], mine[at + tpr]);
         }
-      if (p.gate.data) {
-        stage_param<VEC, NV>(p.gate.data, p.param_dtype, grow * p.gate.ld, t, tpr, p.cols, mine,
-                             tpr);
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = (v * 8 + 2 * i) * tpr;
-            q[v][i] = mul2(q[v][i], pair(mine[at], mine[at + tpr]));
-          }
-      }
     }
     in.begin();
     const float r1 = in.r1, r2 = in.r2;
@@ -745,16 +776,19 @@ __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
       if (c >= p.cols) continue;
       if (p.dw_pre)
         part_row(p, blockIdx.x, kPartWPre)[c] = i & 1 ? lane1(acc[v][i / 2]) : lane0(acc[v][i / 2]);
-      if (p.dw_post) part_row(p, blockIdx.x, kPartWPost)[c] = post[(v * 8 + i) * tpr];
+      const float x = i & 1 ? lane1(e[v][i / 2]) : lane0(e[v][i / 2]);
+      part_row(p, blockIdx.x, kPartWPost)[c] =
+          p.gate_rows == 0 ? p.branch_scale * x : post[(v * 8 + i) * tpr];
     }
 }
 
-// Adds the parts' partial rows.  blockIdx.y: 0 dw_pre, 1 dw_post, from 2 on the
-// gate rows that cross a part's border: gate row blockIdx.y - 2 (when there are
+// Adds the parts' partial rows.  blockIdx.y: 0 dw_pre; 1 dw_post (with one gate row
+// for all rows the sums e, from which dw_post = gate e and dgate = w_post e); from 2 on
+// the gate rows that cross a part's border: gate row blockIdx.y - 2 (when there are
 // fewer gate rows than parts), or the one that begins in part blockIdx.y - 2 and
-// reaches into the next.  32 columns x 16 runs of parts per CTA; a run adds its
+// reaches into the next.  32 columns x 32 runs of parts per CTA; a run adds its
 // parts in order, then the runs' sums are added in order.
-constexpr int kFinishRuns = 16;
+constexpr int kFinishRuns = 32;
 
 __global__ void __launch_bounds__(32 * kFinishRuns)
     block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
@@ -765,24 +799,23 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
   const int64_t parts = p.parts, per = p.per;
   int64_t first = 0, last = parts, out_row = 0;  // parts [first, last)
   int slot = blockIdx.y, first_slot = slot;
-  void* out = blockIdx.y == 0 ? p.dw_pre : p.dw_post;
+  const bool both = blockIdx.y == 1 && p.gate_rows == 0;
+  bool wanted = blockIdx.y == 0 ? p.dw_pre != nullptr
+                                : p.dw_post != nullptr || (both && p.dgate.data != nullptr);
   if (blockIdx.y >= 2) {
-    out = p.dgate.data;
     slot = first_slot = kPartGateFirst;
-    if (p.rows > 0) {
-      const int64_t q = blockIdx.y - 2;
-      const int64_t row = p.by_gate ? q * p.gate_rows : min(p.rows, (q + 1) * per) - 1;
-      int64_t glo, ghi;
-      gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
-      first = glo / per;
-      last = (ghi + per - 1) / per;
-      out_row = gate_row_of(p.gate_rows, row);
-      // inside one part: stored there; found in an earlier part: that one's
-      if (last - first == 1 || (!p.by_gate && first != q)) out = nullptr;
-      if (gate_row_of(p.gate_rows, first * per) != out_row) first_slot = kPartGateLast;
-    }
+    const int64_t q = blockIdx.y - 2;
+    const int64_t row = p.by_gate ? q * p.gate_rows : min(p.rows, (q + 1) * per) - 1;
+    int64_t glo, ghi;
+    gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
+    first = glo / per;
+    last = (ghi + per - 1) / per;
+    out_row = gate_row_of(p.gate_rows, row);
+    // inside one part: stored there; found in an earlier part: that one's
+    wanted = last - first > 1 && (p.by_gate || first == q);
+    if (gate_row_of(p.gate_rows, first * per) != out_row) first_slot = kPartGateLast;
   }
-  if (!out) return;
+  if (!wanted) return;
   float s = 0.f;
   const int64_t each = (last - first + kFinishRuns - 1) / kFinishRuns;
   int64_t a = first + run * each;
@@ -799,10 +832,20 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
   if (run != 0 || col >= p.cols) return;
 #pragma unroll
   for (int i = 1; i < kFinishRuns; ++i) s += run_sum[i][lane];
-  if (blockIdx.y < 2)
-    st_any(out, p.param_dtype, col, s);
-  else
-    st_any(out, p.param_dtype, out_row * p.dgate.ld + col, s);
+  if (blockIdx.y == 0) {
+    st_any(p.dw_pre, p.param_dtype, col, s);
+  } else if (both) {
+    if (p.dw_post)
+      st_any(p.dw_post, p.param_dtype, col,
+             p.gate.data ? s * ld_any(p.gate.data, p.param_dtype, col) : s);
+    if (p.dgate.data)
+      st_any(p.dgate.data, p.param_dtype, col,
+             p.w_post ? s * ld_any(p.w_post, p.param_dtype, col) : s);
+  } else if (blockIdx.y == 1) {
+    st_any(p.dw_post, p.param_dtype, col, s);
+  } else {
+    st_any(p.dgate.data, p.param_dtype, out_row * p.dgate.ld + col, s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1082,17 +1125,15 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
                                            : launch_join_grad<float>(p, vec, st));
   }
   if (!p.dw_pre && !p.dw_post && !p.dgate.data) return DPOPT_OK;
-  // gate rows that cross a part's border: one for all rows, or at most one per
-  // border (none when the parts are whole numbers of gate rows)
+  // gate rows that cross a part's border (none when the parts are whole numbers of
+  // gate rows); one gate row for all rows goes with dw_post
   unsigned gate_sums = 0;
-  if (p.dgate.data) {
+  if (p.dgate.data && rows > 0 && a->gate_rows > 0 && p.per % a->gate_rows != 0) {
     p.by_gate = gates <= parts;
-    if (a->gate_rows == 0)
-      gate_sums = rows == 0 || parts > 1;
-    else if (rows > 0 && p.per % a->gate_rows != 0)
-      gate_sums = (unsigned)(p.by_gate ? gates : parts - 1);
+    gate_sums = (unsigned)(p.by_gate ? gates : parts - 1);
   }
-  if (!p.dw_pre && !p.dw_post && gate_sums == 0) return DPOPT_OK;
+  if (!p.dw_pre && !p.dw_post && gate_sums == 0 && !(p.dgate.data && a->gate_rows == 0))
+    return DPOPT_OK;
   const dim3 grid((unsigned)((cols + 31) / 32), 2 + gate_sums);
   return launched(launch_pdl(block_join_finish_kernel, grid, dim3(32 * kFinishRuns), 0,
                              (cudaStream_t)stream, p),
