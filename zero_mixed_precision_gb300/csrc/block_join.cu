@@ -106,13 +106,15 @@ __host__ __device__ inline int64_t gate_row_of(int64_t gate_rows, int64_t row) {
 // parameters are kept as branch_scale * gate * w_post and w_pre.
 constexpr int kRowCta = 1024;
 
-template <class T, bool VEC, int NV>
-__global__ void __launch_bounds__(kRowCta, 1)
+// TPR: the CTA's threads when they are known at compile time (the element form,
+// whose columns are then at fixed distances), else 0.
+template <class T, bool VEC, int NV, int TPR>
+__global__ void __launch_bounds__(TPR == 0 ? kRowCta : TPR < 512 ? 512 : TPR, 1)
     block_join_kernel(const __grid_constant__ JoinParams p) {
   pdl_enter();
   __shared__ float slot[2][kRowCta / 32][1];
   extern __shared__ float stage[];  // 8 NV places per thread
-  const int t = threadIdx.x, tpr = blockDim.x;
+  const int t = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x;
   const int cols = p.cols;
   if (!dbg_ok(p.dbg, tpr * 8 * NV >= cols)) return;
   const float inv_c = 1.f / (float)cols;
@@ -306,7 +308,7 @@ __device__ __forceinline__ void lanes8(const uint64_t (&f)[4], float (&x)[8]) {
 // zeros throughout.
 template <class T, int YP, int HP>
 struct VecRows {
-  static constexpr int NV = kGradFrags, kMaxThreads = kGradCta;
+  static constexpr int NV = kGradFrags, kMaxThreads = kGradCta, kThreads = 0;
   static constexpr uint32_t kWide = 8 * sizeof(T), kNarrow = 8;
   static constexpr uint32_t kYBytes = YP ? kNarrow : kWide, kHBytes = HP == 2 ? kNarrow : kWide;
   const JoinGradParams& p;
@@ -486,16 +488,19 @@ struct VecRows {
 };
 
 // Element form: straight from global memory, the second reading of a row from L1.
-template <class T, int NV_>
+// The CTA's size is fixed at compile time, and with it the distances between a
+// thread's columns.
+template <class T, int NV_, int TPR>
 struct ElemRows {
-  static constexpr int NV = NV_, kMaxThreads = kRowCta;
+  static constexpr int NV = NV_, kMaxThreads = TPR < 512 ? 512 : TPR, kThreads = TPR;
+  static constexpr int tpr = TPR;
   const JoinGradParams& p;
-  const int t, tpr;
+  const int t;
   int64_t row;
   float r1 = 0.f, r2 = 1.f;
 
   __device__ __forceinline__ ElemRows(const JoinGradParams& q, int64_t lo, int64_t, uint32_t)
-      : p(q), t(threadIdx.x), tpr(blockDim.x), row(lo) {}
+      : p(q), t(threadIdx.x), row(lo) {}
   __device__ __forceinline__ void begin() {
     if (p.du.data) r1 = p.rstd_pre[row];
     if (p.rstd_post) r2 = p.rstd_post[row];
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
   constexpr int NV = Rows::NV;
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float slot[2][Rows::kMaxThreads / 32][3];
-  const int t = threadIdx.x, tpr = blockDim.x;
+  const int t = threadIdx.x, tpr = Rows::kThreads > 0 ? Rows::kThreads : blockDim.x;
   const int64_t lo = blockIdx.x * p.per, hi = min(p.rows, lo + p.per);
   if (!dbg_ok(p.dbg, tpr * 8 * NV >= p.cols && lo < hi)) return;
   const float inv_c = 1.f / (float)p.cols;
@@ -884,10 +889,10 @@ bool vec_ok(const Act8Out& a) { return !a.codes || a.vec; }
 
 constexpr size_t kJoinSmem = 220 * 1024;  // of 227 KB; the static arrays need some
 
-template <class T, bool VEC, int NV>
+template <class T, bool VEC, int NV, int TPR>
 int launch_join_at(JoinParams& p, cudaStream_t stream) {
-  constexpr auto kern = block_join_kernel<T, VEC, NV>;
-  p.tpr = row_threads(p.cols, NV);
+  constexpr auto kern = block_join_kernel<T, VEC, NV, TPR>;
+  p.tpr = TPR > 0 ? TPR : row_threads(p.cols, NV);
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   const size_t smem = (size_t)p.tpr * 8 * NV * sizeof(float);
@@ -907,11 +912,31 @@ int launch_join_at(JoinParams& p, cudaStream_t stream) {
   return launched(launch_pdl(kern, grid, p.tpr, smem, stream, p), "block join");
 }
 
+// The element form's CTA: the smallest of these that covers a row.
+template <template <int, int> class F, class... Args>
+int by_width(int cols, Args&&... args) {
+  if (cols <= 8 * 64) return F<1, 64>::run(args...);
+  if (cols <= 8 * 128) return F<1, 128>::run(args...);
+  if (cols <= 8 * 256) return F<1, 256>::run(args...);
+  if (cols <= 8 * 512) return F<1, 512>::run(args...);
+  if (cols <= 8 * 1024) return F<1, 1024>::run(args...);
+  return F<2, 1024>::run(args...);
+}
+
+template <class T>
+struct ElemJoin {
+  template <int NV, int TPR>
+  struct At {
+    static int run(JoinParams& p, cudaStream_t stream) {
+      return launch_join_at<T, false, NV, TPR>(p, stream);
+    }
+  };
+};
+
 template <class T>
 int launch_join(JoinParams& p, bool vec, cudaStream_t stream) {
-  if (vec) return launch_join_at<T, true, 1>(p, stream);
-  return p.cols <= 8 * kRowCta ? launch_join_at<T, false, 1>(p, stream)
-                               : launch_join_at<T, false, 2>(p, stream);
+  if (vec) return launch_join_at<T, true, 1, 0>(p, stream);
+  return by_width<ElemJoin<T>::template At>(p.cols, p, stream);
 }
 
 template <class T, bool VEC, class Rows>
@@ -923,13 +948,16 @@ int launch_grad_at(JoinGradParams& p, size_t smem, cudaStream_t stream) {
 }
 
 template <class T>
-int launch_grad_elem(JoinGradParams& p, cudaStream_t stream) {
-  const int nv = p.cols <= 8 * kRowCta ? 1 : 2;
-  p.tpr = row_threads(p.cols, nv);
-  const size_t sums = (size_t)p.tpr * 16 * nv * sizeof(float);
-  return nv == 1 ? launch_grad_at<T, false, ElemRows<T, 1>>(p, sums, stream)
-                 : launch_grad_at<T, false, ElemRows<T, 2>>(p, sums, stream);
-}
+struct ElemGrad {
+  template <int NV, int TPR>
+  struct At {
+    static int run(JoinGradParams& p, cudaStream_t stream) {
+      p.tpr = TPR;
+      return launch_grad_at<T, false, ElemRows<T, NV, TPR>>(
+          p, (size_t)TPR * 16 * NV * sizeof(float), stream);
+    }
+  };
+};
 
 template <class T, int YP, int HP>
 int launch_grad_vec(JoinGradParams& p, cudaStream_t stream) {
@@ -939,14 +967,14 @@ int launch_grad_vec(JoinGradParams& p, cudaStream_t stream) {
   const size_t sums = (size_t)p.tpr * 16 * Rows::NV * sizeof(float);
   p.stage_bytes = Rows::stage_bytes(p.tpr);
   // the ring needs room for at least one row
-  if (sums + p.stage_bytes > room) return launch_grad_elem<T>(p, stream);
+  if (sums + p.stage_bytes > room) return by_width<ElemGrad<T>::template At>(p.cols, p, stream);
   p.stages = (int)std::min<size_t>(3, (room - sums) / p.stage_bytes);
   return launch_grad_at<T, true, Rows>(p, sums + p.stages * (size_t)p.stage_bytes, stream);
 }
 
 template <class T>
 int launch_join_grad(JoinGradParams& p, bool vec, cudaStream_t stream) {
-  if (!vec) return launch_grad_elem<T>(p, stream);
+  if (!vec) return by_width<ElemGrad<T>::template At>(p.cols, p, stream);
   if (!p.du.data)
     return p.y8.codes ? launch_grad_vec<T, 1, 0>(p, stream) : launch_grad_vec<T, 0, 0>(p, stream);
   if (p.h8.codes)
