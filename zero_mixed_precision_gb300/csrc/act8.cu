@@ -5,113 +5,51 @@
 namespace dpopt {
 namespace {
 
-// The work is cut into units of 256 columns of a row, one for a warp; a warp's
-// next unit is `step` further on, taken as whole rows and units so that no unit
-// needs a division.
 struct Act8Params {
   int64_t rows;
-  int cols, units;  // units of a row
-  int64_t step_rows;
-  int step_units;
+  int cols;
+  UnitSteps steps;
   Mat x;
   Act8Out packed;
   Dbg dbg;
 };
 
-constexpr int kActThreads = 256, kActUnit = 256;
-
-struct UnitWalk {
-  int64_t row;
-  int unit;
-  __device__ __forceinline__ explicit UnitWalk(const Act8Params& p) {
-    const int64_t first = ((int64_t)blockIdx.x * kActThreads + threadIdx.x) >> 5;
-    row = first / p.units;
-    unit = (int)(first - row * p.units);
-  }
-  __device__ __forceinline__ void next(const Act8Params& p) {
-    row += p.step_rows;
-    unit += p.step_units;
-    if (unit >= p.units) {
-      unit -= p.units;
-      ++row;
-    }
-  }
-};
+constexpr int kActThreads = 256;
 
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kActThreads)
     act8_pack_kernel(const __grid_constant__ Act8Params p) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  UnitWalk at(p);
+  UnitWalk at(p.steps, kActThreads);
   Frag<T, VEC> ahead;
-  if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kActUnit);
-  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.units)) {
+  if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kUnitCols);
+  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.steps.units)) {
     const int64_t row = at.row;
-    const int c0 = at.unit * kActUnit;
+    const int c0 = at.unit * kUnitCols;
     float f[8];
     ahead.widen(f);
-    at.next(p);
-    if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kActUnit);
+    at.next(p.steps);
+    if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kUnitCols);
     frag_pack<T, VEC>(p.packed, row, 0, lane, 32, p.cols, f, c0);
   }
 }
-
-// The vector form: a thread's 8 columns at once; the element form: each lane its
-// column of the unit's 8 blocks.
-template <bool VEC>
-struct CodeFrag;
-template <>
-struct CodeFrag<true> {
-  uint2 c;
-  uint32_t byte;
-  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
-    const int col = c0 + lane * 8;
-    c = make_uint2(0, 0);
-    byte = 0;
-    if (col >= cols) return;
-    c = *reinterpret_cast<const uint2*>(o.codes + row * o.ld_codes + col);
-    byte = o.exps[row * o.ld_exps + col / kAct8Block];
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    act8_values(c, act8_scale(byte), f);
-  }
-};
-template <>
-struct CodeFrag<false> {
-  int8_t c[8];
-  uint8_t byte[8];
-  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
-    const int8_t* codes = o.codes + row * o.ld_codes;
-    const uint8_t* exps = o.exps + row * o.ld_exps;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = c0 + i * 32 + lane;
-      c[i] = col < cols ? codes[col] : 0;
-      byte[i] = col < cols ? exps[col / kAct8Block] : 0;
-    }
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)c[i] * act8_scale(byte[i]);
-  }
-};
 
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kActThreads)
     act8_unpack_kernel(const __grid_constant__ Act8Params p) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  UnitWalk at(p);
+  UnitWalk at(p.steps, kActThreads);
   CodeFrag<VEC> ahead;
-  if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kActUnit);
-  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.units)) {
+  if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kUnitCols);
+  while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.steps.units)) {
     const int64_t row = at.row;
-    const int c0 = at.unit * kActUnit;
+    const int c0 = at.unit * kUnitCols;
     float f[8];
     ahead.values(f);
-    at.next(p);
-    if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kActUnit);
+    at.next(p.steps);
+    if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kUnitCols);
     frag_store<T, VEC>(p.x, row, 0, lane, 32, p.cols, f, c0);
   }
 }
@@ -127,10 +65,9 @@ int prepare(Act8Params& p, bool pack, void* x, int dtype, int64_t rows, int64_t 
   DPOPT_TRY(take_act8("the packed matrix", dpopt_act8{codes, ld_codes, exps, ld_exps}, rows, cols,
                       pack, &p.packed, s, &n));
   DPOPT_TRY(check_overlaps(s, n));
-  if (cols > INT32_MAX - kActUnit) return fail(DPOPT_ERR_UNSUPPORTED, "cols must be below 2^31");
+  if (cols > INT32_MAX - kUnitCols) return fail(DPOPT_ERR_UNSUPPORTED, "cols must be below 2^31");
   p.rows = rows;
   p.cols = (int)cols;
-  p.units = (int)((cols + kActUnit - 1) / kActUnit);
   p.dbg = make_dbg();
   return DPOPT_OK;
 }
@@ -141,12 +78,7 @@ int run(Kernel vec, Kernel elem, Act8Params& p, const char* what, cudaStream_t s
   if (p.rows == 0 || p.cols == 0) return DPOPT_OK;
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
-  constexpr int kWarps = kActThreads / 32;
-  const int64_t ctas = (p.rows * p.units + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8);
-  const int64_t step = (int64_t)grid * kWarps;
-  p.step_rows = step / p.units;
-  p.step_units = (int)(step % p.units);
+  const unsigned grid = unit_grid(p.rows, p.cols, sms * 8, kActThreads, &p.steps);
   const bool v = p.cols % 8 == 0 && p.x.vec && p.packed.vec;
   return launched(launch_pdl(v ? vec : elem, grid, kActThreads, 0, stream, p), what);
 }

@@ -24,60 +24,56 @@ namespace {
 struct OperandParams {
   int64_t tokens;
   int n, k;
-  int64_t x_units, units;  // warp units of 256 columns: the packed input's, and dy's after them
+  UnitSteps x_steps, dy_steps;
+  int copy_dy;  // dy's rows are not aligned for the tensor copies
   Act8Out x;
   Mat dy;
-  void *x_out, *dy_out;
-  int64_t ld_x, ld_dy;  // row strides of the copies, multiples of 8
+  Mat x_out, dy_out;  // rows of whole 128 bytes
   Dbg dbg;
 };
 
-constexpr int kOperandThreads = 256, kUnit = 256;
+constexpr int kOperandThreads = 256;
 
-template <class T>
+template <class T, bool VEC>
 __global__ void __launch_bounds__(kOperandThreads)
     act8_operands_kernel(const __grid_constant__ OperandParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const int xu = (p.k + kUnit - 1) / kUnit, du = (p.n + kUnit - 1) / kUnit;
-  const bool vec = p.x.vec && p.k % 8 == 0;
-  for (int64_t w = ((int64_t)blockIdx.x * kOperandThreads + threadIdx.x) >> 5; w < p.units;
-       w += (int64_t)gridDim.x * (kOperandThreads / 32)) {
-    if (w < p.x_units) {
-      const int64_t row = w / xu;
-      const int c0 = (int)(w - row * xu) * kUnit;
-      if (!dbg_ok(p.dbg, row < p.tokens)) continue;
-      const int8_t* codes = p.x.codes + row * p.x.ld_codes;
-      const uint8_t* exps = p.x.exps + row * p.x.ld_exps;
-      T* out = static_cast<T*>(p.x_out) + row * p.ld_x;
-      if (vec) {
-        const int c = c0 + lane * 8;
-        if (c >= p.k) continue;
-        float f[8];
-        act8_values(*reinterpret_cast<const uint2*>(codes + c), act8_scale(exps[c / kAct8Block]),
-                    f);
-        *reinterpret_cast<uint4*>(out + c) =
+  UnitWalk at(p.x_steps, kOperandThreads);
+  CodeFrag<VEC> ahead;
+  if (at.row < p.tokens) ahead.load(p.x, at.row, lane, p.k, at.unit * kUnitCols);
+  while (at.row < p.tokens && dbg_ok(p.dbg, at.unit < p.x_steps.units)) {
+    const int64_t row = at.row;
+    const int c0 = at.unit * kUnitCols;
+    float f[8];
+    ahead.values(f);
+    at.next(p.x_steps);
+    if (at.row < p.tokens) ahead.load(p.x, at.row, lane, p.k, at.unit * kUnitCols);
+    T* out = static_cast<T*>(p.x_out.data) + row * p.x_out.ld + c0;
+    if constexpr (VEC) {
+      if (c0 + lane * 8 < p.k)  // the product reads it next: kept in L2
+        *reinterpret_cast<uint4*>(out + lane * 8) =
             make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
                        pack2(f[6], f[7], T()));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0 + i * 32 + lane;
-          if (c < p.k) out[c] = from_f32<T>((float)codes[c] * act8_scale(exps[c / kAct8Block]));
-        }
-      }
     } else {
-      const int64_t row = (w - p.x_units) / du;
-      const int c0 = (int)(w - p.x_units - row * du) * kUnit;
-      if (!dbg_ok(p.dbg, row < p.tokens)) continue;
-      const T* in = static_cast<const T*>(p.dy.data) + row * p.dy.ld;
-      T* out = static_cast<T*>(p.dy_out) + row * p.ld_dy;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = c0 + i * 32 + lane;
-        if (c < p.n) out[c] = in[c];
-      }
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i * 32 + lane < p.k) out[i * 32 + lane] = from_f32<T>(f[i]);
     }
+  }
+  if (!p.copy_dy) return;
+  for (UnitWalk u(p.dy_steps, kOperandThreads);
+       u.row < p.tokens && dbg_ok(p.dbg, u.unit < p.dy_steps.units); u.next(p.dy_steps)) {
+    const int c0 = u.unit * kUnitCols;
+    const T* in = static_cast<const T*>(p.dy.data) + u.row * p.dy.ld + c0;
+    T* out = static_cast<T*>(p.dy_out.data) + u.row * p.dy_out.ld + c0;
+    T x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i * 32 + lane < p.n) x[i] = in[i * 32 + lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i * 32 + lane < p.n) out[i * 32 + lane] = x[i];
   }
 }
 
@@ -766,23 +762,30 @@ int run_wgrad(const Plan& plan, GemmParams& g, OperandParams& o, unsigned char* 
   constexpr bool is_bf16 = std::is_same_v<T, bf16>;
   // dy is read in place when its rows are aligned for the copies
   const bool in_place = (uintptr_t)o.dy.data % 16 == 0 && o.dy.ld % 8 == 0;
-  o.x_out = scratch;
-  o.dy_out = scratch + plan.x_bytes;
-  o.ld_x = plan.ld_x;
-  o.ld_dy = plan.ld_dy;
-  o.x_units = o.tokens * ((o.k + kUnit - 1) / kUnit);
-  o.units = o.x_units + (in_place ? 0 : o.tokens * ((o.n + kUnit - 1) / kUnit));
+  o.x_out = Mat{scratch, plan.ld_x, 1};
+  o.dy_out = Mat{scratch + plan.x_bytes, plan.ld_dy, 1};
+  o.copy_dy = !in_place;
   g.partial = reinterpret_cast<float*>(scratch + plan.x_bytes + plan.dy_bytes);
   int sms = 0;
   DPOPT_TRY(sm_count(&sms));
   CUtensorMap a, b;
   DPOPT_TRY(in_place ? encode(&a, is_bf16, o.dy.data, o.n, o.tokens, o.dy.ld)
-                     : encode(&a, is_bf16, o.dy_out, o.n, o.tokens, o.ld_dy));
-  DPOPT_TRY(encode(&b, is_bf16, o.x_out, o.k, o.tokens, o.ld_x));
-  const unsigned ctas = (unsigned)std::min<int64_t>((o.units + 7) / 8, (int64_t)sms * 8);
-  DPOPT_TRY(launched(
-      launch_pdl(act8_operands_kernel<T>, ctas, kOperandThreads, 0, stream, o),
-      "act8 weight gradient operands"));
+                     : encode(&a, is_bf16, o.dy_out.data, o.n, o.tokens, plan.ld_dy));
+  DPOPT_TRY(encode(&b, is_bf16, scratch, o.k, o.tokens, plan.ld_x));
+  // one grid for both walks
+  unsigned ctas = unit_grid(o.tokens, o.k, (int64_t)sms * 8, kOperandThreads, &o.x_steps);
+  if (o.copy_dy) {
+    UnitSteps unused;
+    const unsigned want =
+        unit_grid(o.tokens, std::max(o.n, o.k), (int64_t)sms * 8, kOperandThreads, &unused);
+    ctas = std::max(ctas, want);
+    set_steps(ctas, kOperandThreads, o.k, &o.x_steps);
+    set_steps(ctas, kOperandThreads, o.n, &o.dy_steps);
+  }
+  const bool vec = o.x.vec && o.k % 8 == 0;
+  DPOPT_TRY(launched(launch_pdl(vec ? act8_operands_kernel<T, true> : act8_operands_kernel<T, false>,
+                                ctas, kOperandThreads, 0, stream, o),
+                     "act8 weight gradient operands"));
   if (g.out_dtype == DPOPT_GRAD_F32)
     return plan.pair ? launch_gemm<T, 2, 256, true>(g, a, b, stream)
                      : launch_gemm<T, 1, 128, true>(g, a, b, stream);

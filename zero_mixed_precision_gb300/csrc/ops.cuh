@@ -374,6 +374,88 @@ __device__ __forceinline__ void round8(const float (&f)[8], float (&r)[8]) {
   for (int i = 0; i < 8; ++i) r[i] = to_f32(from_f32<T>(f[i]));
 }
 
+// Matrices walked by warps in units of 256 columns of a row.  A warp's next unit is
+// as many units further on as the grid has warps, taken as whole rows and units,
+// so that only the first needs a division (a 64-bit division per unit cost as much
+// as packing it).
+constexpr int kUnitCols = 256;
+
+struct UnitSteps {
+  int64_t rows;      // whole rows of a step
+  int rest, units;   // and units beyond them; units of a row
+};
+
+inline void set_steps(int64_t ctas, int threads, int64_t cols, UnitSteps* s) {
+  s->units = (int)((cols + kUnitCols - 1) / kUnitCols);
+  s->rows = ctas * (threads / 32) / s->units;
+  s->rest = (int)(ctas * (threads / 32) % s->units);
+}
+// The grid for rows x cols (at most `most` CTAs of `threads`) and its steps.
+inline unsigned unit_grid(int64_t rows, int64_t cols, int64_t most, int threads, UnitSteps* s) {
+  const int64_t units = (cols + kUnitCols - 1) / kUnitCols, warps = threads / 32;
+  const int64_t ctas = std::min<int64_t>((rows * units + warps - 1) / warps, most);
+  set_steps(ctas, threads, cols, s);
+  return (unsigned)ctas;
+}
+
+struct UnitWalk {
+  int64_t row;
+  int unit;
+  __device__ __forceinline__ UnitWalk(const UnitSteps& s, int threads) {
+    const int64_t first = ((int64_t)blockIdx.x * threads + threadIdx.x) >> 5;
+    row = first / s.units;
+    unit = (int)(first - row * s.units);
+  }
+  __device__ __forceinline__ void next(const UnitSteps& s) {
+    row += s.rows;
+    unit += s.rest;
+    if (unit >= s.units) {
+      unit -= s.units;
+      ++row;
+    }
+  }
+};
+
+// Packed units on their way to values.  The vector form: a thread's 8 columns at
+// once; the element form: each lane its column of the unit's 8 blocks.
+template <bool VEC>
+struct CodeFrag;
+template <>
+struct CodeFrag<true> {
+  uint2 c;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
+    const int col = c0 + lane * 8;
+    c = make_uint2(0, 0);
+    byte = 0;
+    if (col >= cols) return;
+    c = *reinterpret_cast<const uint2*>(o.codes + row * o.ld_codes + col);
+    byte = o.exps[row * o.ld_exps + col / kAct8Block];
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    act8_values(c, act8_scale(byte), f);
+  }
+};
+template <>
+struct CodeFrag<false> {
+  int8_t c[8];
+  uint8_t byte[8];
+  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
+    const int8_t* codes = o.codes + row * o.ld_codes;
+    const uint8_t* exps = o.exps + row * o.ld_exps;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = c0 + i * 32 + lane;
+      c[i] = col < cols ? codes[col] : 0;
+      byte[i] = col < cols ? exps[col / kAct8Block] : 0;
+    }
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)c[i] * act8_scale(byte[i]);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // bounds checks of the bounds-checked build
 // ---------------------------------------------------------------------------
