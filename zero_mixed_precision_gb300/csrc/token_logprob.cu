@@ -12,7 +12,8 @@ constexpr int kTokWarps = kTokThreads / 32;
 
 // Rows are cut into parts, one CTA each, when there are too few rows to fill
 // the GPU: about kTokCtas CTAs in all, none below kTokPartMin elements.  A
-// function of the sizes alone, so results do not depend on the GPU.
+// function of the sizes alone, so results do not depend on the GPU.  One row of
+// 131072 takes 7.7 us in 64 parts and a join, 357 us in one CTA of the first form.
 constexpr int kTokCtas = 512, kTokPartMin = 2048, kTokMaxParts = 64;
 
 __host__ __device__ inline int64_t tok_parts(int64_t rows, int64_t vocab) {
@@ -201,7 +202,7 @@ struct TokShared {
   uint64_t kslot[kTokWarps];
   uint32_t group[32], floor;
   int found, agains;
-  uint8_t again[kTokThreads];
+  uint16_t again[kTokThreads];
   uint64_t cand[1024];
   uint64_t best[DPOPT_MAX_TOP];
 };
@@ -251,17 +252,18 @@ __device__ __forceinline__ void top_by_passes(int top, uint64_t* best, TokShared
 
 // The `top` largest keys of a stretch, into sh.best (zeros where it has fewer).
 // thread_max is the largest logit this thread saw: the top-th largest of the
-// 32 maxima over eight threads each is a floor that at least `top` elements
+// maxima over 32 groups of threads is a floor that at least `top` elements
 // reach, and only threads whose own maximum reaches it look at their elements
-// again (about `top` threads of the 256).
+// again (about `top` of them).
 template <class T>
 __device__ void stretch_top(const Stretch<T>& st, int64_t lo, int top, float thread_max,
                             TokShared& sh) {
   const uint32_t mine = rank_bits(thread_max);
   uint32_t g = mine;
+  constexpr int kGroup32 = kTokThreads / 32;  // threads of one of 32 groups
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-  if ((threadIdx.x & 7) == 0) sh.group[threadIdx.x >> 3] = g;
+  for (int o = 1; o < kGroup32; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if (threadIdx.x % kGroup32 == 0) sh.group[threadIdx.x / kGroup32] = g;
   if (threadIdx.x == 0) sh.found = sh.agains = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -284,7 +286,7 @@ __device__ void stretch_top(const Stretch<T>& st, int64_t lo, int top, float thr
   };
   // the threads to look at again, then a warp for each: lane i takes the thread's
   // i-th vector, so that they are all in flight at once
-  if (mine >= floor) sh.again[atomicAdd(&sh.agains, 1)] = (uint8_t)threadIdx.x;
+  if (mine >= floor) sh.again[atomicAdd(&sh.agains, 1)] = (uint16_t)threadIdx.x;
   __syncthreads();
   const int agains = sh.agains, lane = threadIdx.x & 31;
   for (int a = threadIdx.x >> 5; a < agains; a += kTokWarps) {
@@ -366,7 +368,11 @@ __device__ void finish_row(const LogprobParams& p, int64_t row, const T* x, TokP
 }
 
 // One CTA per part of a row: one pass with a running softmax per thread, four
-// vectors in flight.
+// vectors in flight.  Bound by reading the logits once; the alternatives cost 19 us
+// of 8192 x 50257 bf16's 145 us (5.67 TB/s, 84 % of the measured copy rate; 126 us,
+// 96 %, without them): their few loads and barriers between a row's last vector
+// and its results.  Lists kept while reading (a sorted list per warp) would have cost five
+// times the pass's own instructions.
 template <class T>
 __global__ void __launch_bounds__(kTokThreads) token_logprob_kernel(const __grid_constant__ LogprobParams p) {
   pdl_enter();
@@ -463,11 +469,14 @@ struct LogprobGradParams {
 // held above -1e4, where 2^q is 0 in fp32: a masked entry gives 0 and no product
 // overflows.  With one token per row (ONE) its element is met on the way; more
 // are stored again after a barrier, from logits read before it (dlogits may be
-// the logits).
-constexpr int64_t kGradStretch = 4 * kTokThreads * 8;
+// the logits).  Reads and writes every logit once: 8192 x 50304 fp16 in 237 us, 6.96
+// TB/s, the copy rate; with a barrier before the first vector was used it took
+// 360 us, a row's loads waiting for its tokens.
+constexpr int kGradThreads = 256;
+constexpr int64_t kGradStretch = 4 * kGradThreads * 8;
 
 template <class T, bool ONE>
-__global__ void __launch_bounds__(kTokThreads, 5)
+__global__ void __launch_bounds__(kGradThreads, 5)
 token_logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
   pdl_enter();
   __shared__ int64_t tok[ONE ? 1 : DPOPT_MAX_TOKENS];
@@ -484,7 +493,7 @@ token_logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
   Raw8<T> r[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int v = threadIdx.x + u * kTokThreads;
+    const int v = threadIdx.x + u * kGradThreads;
     if (v < vecs) r[u] = ld_raw8<T>(body + v * 8);
   }
   const float scale = (p.loss_scale ? p.loss_scale->scale : 1.f) * p.inv_temp;
@@ -524,7 +533,7 @@ token_logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
   };
   // a given token's own term, unless its entry is masked
   auto own = [&](float v, float g, float d) { return v == -INFINITY || zero ? g : fmaf(scale, d, g); };
-  for (int64_t t = threadIdx.x; t < st.loose(); t += kTokThreads) {
+  for (int64_t t = threadIdx.x; t < st.loose(); t += kGradThreads) {
     const int64_t j = st.loose_at(t);
     const float v = to_f32(st.x[j]);
     float g = grad(v);
@@ -565,7 +574,7 @@ token_logprob_grad_kernel(const __grid_constant__ LogprobGradParams p) {
   };
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int v = threadIdx.x + u * kTokThreads;
+    const int v = threadIdx.x + u * kGradThreads;
     if (v < vecs) eight(r[u], v);
   }
   if constexpr (!ONE) {
@@ -767,7 +776,7 @@ int dpopt_token_logprob_backward(const void* logits, int dtype, int64_t rows, in
                          : token_logprob_grad_kernel<fp16, false>)
                   : (one ? token_logprob_grad_kernel<float, true>
                          : token_logprob_grad_kernel<float, false>);
-  return launched(launch_pdl(kern, (unsigned)(rows * p.stretches), kTokThreads, 0,
+  return launched(launch_pdl(kern, (unsigned)(rows * p.stretches), kGradThreads, 0,
                              (cudaStream_t)stream, p),
                   "token logprob gradient");
 }
