@@ -6,7 +6,8 @@
 // largest magnitude, one fused multiply-add per two codes that scales and rounds,
 // byte permutes).  A warp takes 256 columns of a row, the next unit's loads in
 // flight while it works on one.  8192 x 8192 bf16: 36.7 us packing, 35.8 us restoring,
-// 5.5 and 5.7 TB/s (82 and 84 % of the measured copy rate); fp32 6.2 TB/s packing.
+// 5.5 and 5.7 TB/s (82 and 84 % of the measured copy rate); fp32 55 and 64 us, 6.2
+// and 5.2 TB/s (the restoring writes four bytes for each that it reads).
 // Rows that are not 16-byte aligned go element by element, a warp's lanes on
 // neighbouring columns (8192 x 8191: 103 and 90 us).
 #include "ops.cuh"
