@@ -100,6 +100,33 @@ def test_pack_strides_and_alignment(dp, cols, ld, off, ldc, offc, dtype):
         assert bool((buf[keep] == 77).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [1, 9, 255, 257, 515, 1031])
+@pytest.mark.parametrize("pad,off,padc,offc", [(0, 0, 0, 0), (1, 1, 0, 3), (3, 7, 5, 1),
+                                               (6, 2, 2, 6), (8, 5, 8, 7)])
+def test_pack_rows_at_any_alignment(dp, cols, pad, off, padc, offc, dtype):
+    """Rows of several units that start anywhere, between neighbours that are NaN: those
+    neither enter a block nor are written."""
+    rows = 6
+    bufx, x = _padded(rows, cols, cols + pad, dtype, off)
+    bufx.fill_(math.nan)
+    x.copy_(_rand(_gen(cols + pad), rows, cols))
+    bufc, codes = _padded(rows, cols, cols + padc, torch.int8, offc)
+    _, exps = dp.act8_empty(rows, cols)
+    dp.act8_pack(x, codes, exps)
+    want_c, want_e = ref.pack(x)
+    assert torch.equal(codes.cpu(), want_c) and torch.equal(exps.cpu(), want_e)
+    bufb, back = _padded(rows, cols, cols + pad, dtype, off)
+    dp.act8_unpack(codes, exps, back)
+    dp.stream_status()
+    assert torch.equal(back.cpu().double(), ref.unpack(want_c, want_e))
+    for buf, view, w in ((bufc, codes, cols + padc), (bufb, back, cols + pad)):
+        keep = torch.ones_like(buf, dtype=torch.bool)
+        o = view.storage_offset()
+        keep[o:o + rows * w].view(rows, w)[:, :cols] = False
+        assert bool((buf[keep] == 77).all())
+
+
 def test_pack_error_bound_and_exact_restore(dp):
     """|value - x| <= step / 2 (<= step above 127.5 steps), and the restored value is exact in
     the source type: packing it again changes nothing."""
@@ -181,6 +208,12 @@ def test_wgrad_output_types_and_addend(dp, out, add):
 @pytest.mark.parametrize("pad,off", [(8, 0), (24, 0), (1, 0), (8, 1), (13, 5)])
 def test_wgrad_strides_and_alignment(dp, pad, off):
     _wgrad(dp, 150, 256, 320, torch.bfloat16, torch.float32, pad=pad, off=off)
+
+
+@pytest.mark.parametrize("n,k,pad,off", [(515, 321, 0, 0), (301, 777, 4, 3), (8, 257, 1, 7)])
+def test_wgrad_odd_rows(dp, n, k, pad, off):
+    for dtype in DTYPES[:2]:
+        _wgrad(dp, 90, n, k, dtype, torch.float32, pad=pad, off=off)
 
 
 def test_wgrad_adds_in_place(dp):

@@ -8,8 +8,9 @@
 // flight while it works on one.  8192 x 8192 bf16: 36.7 us packing, 35.8 us restoring,
 // 5.5 and 5.7 TB/s (82 and 84 % of the measured copy rate); fp32 55 and 64 us, 6.2
 // and 5.2 TB/s (the restoring writes four bytes for each that it reads).
-// Rows that are not 16-byte aligned go element by element, a warp's lanes on
-// neighbouring columns (8192 x 8191: 103 and 90 us).
+// Rows that are not 16-byte aligned are read and written by whole aligned chunks all
+// the same, shifted between lanes (8192 x 8191: 65 and 61 us; element by element, a
+// warp's lanes on neighbouring columns, they were 103 and 90).
 #include "ops.cuh"
 
 namespace dpopt {
@@ -32,16 +33,16 @@ __global__ void __launch_bounds__(kActThreads)
   pdl_enter();
   const int lane = threadIdx.x & 31;
   UnitWalk at(p.steps, kActThreads);
-  Frag<T, VEC> ahead;
-  if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kUnitCols);
+  UnitFrag<T, VEC> ahead;
+  if (at.row < p.rows) ahead.load(p.x, p.rows, at.row, lane, p.cols, at.unit * kUnitCols);
   while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.steps.units)) {
     const int64_t row = at.row;
     const int c0 = at.unit * kUnitCols;
     float f[8];
-    ahead.widen(f);
+    ahead.widen(f, c0 + lane * 8, p.cols);
     at.next(p.steps);
-    if (at.row < p.rows) ahead.load(p.x, at.row, 0, lane, 32, p.cols, at.unit * kUnitCols);
-    frag_pack<T, VEC>(p.packed, row, 0, lane, 32, p.cols, f, c0);
+    if (at.row < p.rows) ahead.load(p.x, p.rows, at.row, lane, p.cols, at.unit * kUnitCols);
+    unit_pack<T, VEC>(p.packed, row, lane, p.cols, c0, f);
   }
 }
 
@@ -52,15 +53,15 @@ __global__ void __launch_bounds__(kActThreads)
   const int lane = threadIdx.x & 31;
   UnitWalk at(p.steps, kActThreads);
   CodeFrag<VEC> ahead;
-  if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kUnitCols);
+  if (at.row < p.rows) ahead.load(p.packed, p.rows, at.row, lane, p.cols, at.unit * kUnitCols);
   while (at.row < p.rows && dbg_ok(p.dbg, at.unit < p.steps.units)) {
     const int64_t row = at.row;
     const int c0 = at.unit * kUnitCols;
     float f[8];
     ahead.values(f);
     at.next(p.steps);
-    if (at.row < p.rows) ahead.load(p.packed, at.row, lane, p.cols, at.unit * kUnitCols);
-    frag_store<T, VEC>(p.x, row, 0, lane, 32, p.cols, f, c0);
+    if (at.row < p.rows) ahead.load(p.packed, p.rows, at.row, lane, p.cols, at.unit * kUnitCols);
+    unit_store<T, VEC>(p.x, row, lane, p.cols, c0, f);
   }
 }
 

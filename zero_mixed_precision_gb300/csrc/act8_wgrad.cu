@@ -47,39 +47,32 @@ __global__ void __launch_bounds__(kOperandThreads)
   const int lane = threadIdx.x & 31;
   UnitWalk at(p.x_steps, kOperandThreads);
   CodeFrag<VEC> ahead;
-  if (at.row < p.tokens) ahead.load(p.x, at.row, lane, p.k, at.unit * kUnitCols);
+  if (at.row < p.tokens) ahead.load(p.x, p.tokens, at.row, lane, p.k, at.unit * kUnitCols);
   while (at.row < p.tokens && dbg_ok(p.dbg, at.unit < p.x_steps.units)) {
     const int64_t row = at.row;
     const int c0 = at.unit * kUnitCols;
     float f[8];
     ahead.values(f);
     at.next(p.x_steps);
-    if (at.row < p.tokens) ahead.load(p.x, at.row, lane, p.k, at.unit * kUnitCols);
+    if (at.row < p.tokens) ahead.load(p.x, p.tokens, at.row, lane, p.k, at.unit * kUnitCols);
     T* out = static_cast<T*>(p.x_out.data) + row * p.x_out.ld + c0;
-    if constexpr (VEC) {
-      if (c0 + lane * 8 < p.k)  // the product reads it next: kept in L2
-        *reinterpret_cast<uint4*>(out + lane * 8) =
-            make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
-                       pack2(f[6], f[7], T()));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + i * 32 + lane < p.k) out[i * 32 + lane] = from_f32<T>(f[i]);
-    }
+    if (c0 + lane * 8 < p.k)  // the product reads it next: kept in L2; rows are padded
+      *reinterpret_cast<uint4*>(out + lane * 8) =
+          make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
+                     pack2(f[6], f[7], T()));
   }
   if (!p.copy_dy) return;
+  const T* dy = static_cast<const T*>(p.dy.data);
   for (UnitWalk u(p.dy_steps, kOperandThreads);
        u.row < p.tokens && dbg_ok(p.dbg, u.unit < p.dy_steps.units); u.next(p.dy_steps)) {
-    const int c0 = u.unit * kUnitCols;
-    const T* in = static_cast<const T*>(p.dy.data) + u.row * p.dy.ld + c0;
-    T* out = static_cast<T*>(p.dy_out.data) + u.row * p.dy_out.ld + c0;
-    T x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + i * 32 + lane < p.n) x[i] = in[i * 32 + lane];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + i * 32 + lane < p.n) out[i * 32 + lane] = x[i];
+    const int col = u.unit * kUnitCols + lane * 8;
+    if (col >= p.n) continue;
+    Window<16, 2> in;
+    uint32_t w[4];
+    in.load(dy + u.row * p.dy.ld + col, true, dy, dy + (p.tokens - 1) * p.dy.ld + p.n);
+    in.words(w);
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.dy_out.data) + u.row * p.dy_out.ld + col) =
+        make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

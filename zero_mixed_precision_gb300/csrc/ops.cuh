@@ -235,13 +235,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Pack the eight values f of columns col.. of one row, all of them or none below
-// cols.  The four threads of a block's 32 columns (adjacent lanes, the first at a
-// multiple of four) call it together; columns from `cols` on carry zeros and are
-// not stored.
+// The codes (two words) of eight adjacent columns' values f; returns their block's
+// exponent byte.  The four threads of a block's 32 columns (adjacent lanes, the first
+// at a multiple of four) call it together, with zeros for columns that are not there.
 template <class T>
-__device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int col, int cols,
-                                            const float (&f)[8]) {
+__device__ __forceinline__ uint32_t act8_codes8(const float (&f)[8], uint32_t& lo, uint32_t& hi) {
   float m = fabsf(f[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
@@ -250,7 +248,6 @@ __device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int c
   const uint32_t amax = __float_as_uint(m);
   const uint32_t byte = act8_byte<T>(amax);
   const float inv = act8_inverse(byte);
-  uint32_t lo, hi;
   if ((amax & 0x7fffffu) >= 0x7f0000u || byte == 255u) {
     // a value may round to 128 and is clamped (the block's largest is 127.5 steps or
     // more), or the block is not finite
@@ -272,6 +269,15 @@ __device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int c
     lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
   }
+  return byte;
+}
+
+// Pack the eight values f of columns col.. of one row, all of them or none below cols.
+template <class T>
+__device__ __forceinline__ void act8_store8(const Act8Out& o, int64_t row, int col, int cols,
+                                            const float (&f)[8]) {
+  uint32_t lo, hi;
+  const uint32_t byte = act8_codes8<T>(f, lo, hi);
   if (col >= cols) return;
   *reinterpret_cast<uint2*>(o.codes + row * o.ld_codes + col) = make_uint2(lo, hi);
   if ((threadIdx.x & 3) == 0) o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
@@ -437,43 +443,235 @@ struct UnitWalk {
   }
 };
 
-// Packed units on their way to values.  The vector form: a thread's 8 columns at
-// once; the element form: each lane its column of the unit's 8 blocks.
-template <bool VEC>
-struct CodeFrag;
-template <>
-struct CodeFrag<true> {
-  uint2 c;
-  uint32_t byte;
-  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
-    const int col = c0 + lane * 8;
-    c = make_uint2(0, 0);
-    byte = 0;
-    if (col >= cols) return;
-    c = *reinterpret_cast<const uint2*>(o.codes + row * o.ld_codes + col);
-    byte = o.exps[row * o.ld_exps + col / kAct8Block];
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    act8_values(c, act8_scale(byte), f);
-  }
-};
-template <>
-struct CodeFrag<false> {
-  int8_t c[8];
-  uint8_t byte[8];
-  __device__ __forceinline__ void load(const Act8Out& o, int64_t row, int lane, int cols, int c0) {
-    const int8_t* codes = o.codes + row * o.ld_codes;
-    const uint8_t* exps = o.exps + row * o.ld_exps;
+// Rows at any alignment.  A thread's 8 columns are a run of BYTES bytes that starts m
+// bytes into an aligned chunk; m is the same for a whole warp.  A load takes the
+// aligned chunks that hold the run and shifts it out of them; a store takes the
+// bytes before its first chunk's end from the lane before, so that whole chunks
+// are written, and single elements where a row or unit begins or ends.  E is the
+// element's size.
+
+// out = 4 N bytes of w from byte m on (m below 4 (K - N), K - N a power of two).
+template <int N, int K>
+__device__ __forceinline__ void shift_bytes(const uint32_t (&w)[K], int m, uint32_t (&out)[N]) {
+  uint32_t t[K];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = c0 + i * 32 + lane;
-      c[i] = col < cols ? codes[col] : 0;
-      byte[i] = col < cols ? exps[col / kAct8Block] : 0;
+  for (int i = 0; i < K; ++i) t[i] = w[i];
+#pragma unroll
+  for (int s = (K - N) / 2; s > 0; s /= 2) {
+    if (m & (4 * s)) {
+#pragma unroll
+      for (int i = 0; i + s < K; ++i) t[i] = t[i + s];
     }
   }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)c[i] * act8_scale(byte[i]);
+  for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], (m & 3) * 8);
+}
+
+template <int BYTES, int E>
+struct Window {
+  static constexpr int kChunk = BYTES < 16 ? BYTES : 16, kWords = BYTES / 4;
+  static constexpr int kMore = kChunk / 4;
+  uint32_t w[kWords + kMore];
+  int m;
+
+  // The run at p; [lo, hi) is the matrix, outside of which nothing is read (chunks
+  // at its ends by elements; a row's neighbours in it may be read and are
+  // shifted out or left to the caller).
+  __device__ __forceinline__ void load(const void* p, bool any, const void* lo, const void* hi) {
+    const uintptr_t at = (uintptr_t)p;
+    m = (int)(at & (kChunk - 1));
+#pragma unroll
+    for (int i = 0; i < kWords + kMore; ++i) w[i] = 0;
+    if (!any) return;
+#pragma unroll
+    for (int j = 0; j <= BYTES / kChunk; ++j) {
+      if (j == BYTES / kChunk && m == 0) break;
+      const uintptr_t a = at - m + j * kChunk;
+      if (a >= (uintptr_t)lo && a + kChunk <= (uintptr_t)hi) {
+        if constexpr (kChunk == 16) {
+          const uint4 v = *reinterpret_cast<const uint4*>(a);
+          w[j * 4] = v.x, w[j * 4 + 1] = v.y, w[j * 4 + 2] = v.z, w[j * 4 + 3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(a);
+          w[j * 2] = v.x, w[j * 2 + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kChunk; b += E) {
+          const uintptr_t c = a + b;
+          if (c >= (uintptr_t)lo && c < (uintptr_t)hi) {
+            uint32_t v;
+            if constexpr (E == 1) v = *reinterpret_cast<const uint8_t*>(c);
+            if constexpr (E == 2) v = *reinterpret_cast<const uint16_t*>(c);
+            if constexpr (E == 4) v = *reinterpret_cast<const uint32_t*>(c);
+            w[j * kMore + b / 4] |= v << (b % 4 * 8);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void words(uint32_t (&out)[kWords]) const {
+    shift_bytes<kWords>(w, m, out);
+  }
+};
+
+// Store a warp's runs, lane's at p; `left` bytes of the row from p on are there (none
+// or fewer than none for lanes behind its end).
+template <int BYTES, int E>
+__device__ __forceinline__ void store_window(void* p, const uint32_t (&w)[BYTES / 4], int lane,
+                                             int64_t left) {
+  constexpr int C = BYTES < 16 ? BYTES : 16, N = BYTES / 4, M = C / 4;
+  const uintptr_t at = (uintptr_t)p;
+  const int m = (int)(at & (C - 1));
+  uint32_t all[M + N], out[N];
+#pragma unroll
+  for (int i = 0; i < M; ++i) all[i] = __shfl_up_sync(0xffffffffu, w[N - M + i], 1);
+#pragma unroll
+  for (int i = 0; i < N; ++i) all[M + i] = w[i];
+  if (m) {
+    shift_bytes<N>(all, C - m, out);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = w[i];
+  }
+  const auto element = [&](uintptr_t a, uint32_t word) {
+    if constexpr (E == 1) *reinterpret_cast<uint8_t*>(a) = (uint8_t)word;
+    if constexpr (E == 2) *reinterpret_cast<uint16_t*>(a) = (uint16_t)word;
+    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(a) = word;
+  };
+#pragma unroll
+  for (int j = 0; j < BYTES / C; ++j) {
+    const uintptr_t a = at - m + j * C;
+    const int from = j * C - m;  // the chunk's first byte, counted from p
+    if (lane == 0 && from < 0) continue;
+    if (from + C <= left) {
+      if constexpr (C == 16)
+        *reinterpret_cast<uint4*>(a) =
+            make_uint4(out[j * 4], out[j * 4 + 1], out[j * 4 + 2], out[j * 4 + 3]);
+      else
+        *reinterpret_cast<uint2*>(a) = make_uint2(out[j * 2], out[j * 2 + 1]);
+    } else if (from < left) {  // the row ends in it
+#pragma unroll
+      for (int e = 0; e < C; e += E)
+        if (from + e < left) element(a + e, out[(j * C + e) / 4] >> (e % 4 * 8));
+    }
+  }
+  if (m == 0) return;
+  // The run's beginning (lane 0's first C - m bytes) and end (lane 31's last m) share
+  // their chunks with other units: an element a lane, 16 lanes for either.
+  const bool end = lane >= 16;
+  const int b = (lane & 15) * E;
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const uint32_t v = __shfl_sync(0xffffffffu, lane == 31 ? w[N - M + i] : w[i], end ? 31 : 0);
+    if (b / 4 == i) word = v;
+  }
+  const int off = b + (end ? 32 * BYTES - C : 0);  // counted from lane 0's first byte
+  if (b < C && (b >= C - m) == end && off < left + lane * BYTES)
+    element(at - lane * BYTES + off, word >> (b % 4 * 8));
+}
+
+// A warp's unit of 256 columns from c0 on of a row, 8 adjacent columns a lane, on its
+// way to values (zeros from cols on).  VEC: rows may be moved 8 elements at a time.
+template <class T, bool VEC>
+struct UnitFrag {
+  Frag<T, true> f;
+  __device__ __forceinline__ void load(const Mat& m, int64_t, int64_t row, int lane, int cols,
+                                       int c0) {
+    f.load(m, row, 0, lane, 32, cols, c0);
+  }
+  __device__ __forceinline__ void widen(float (&x)[8], int, int) const { f.widen(x); }
+};
+template <class T>
+struct UnitFrag<T, false> {
+  Window<8 * (int)sizeof(T), (int)sizeof(T)> at;
+  __device__ __forceinline__ void load(const Mat& m, int64_t rows, int64_t row, int lane, int cols,
+                                       int c0) {
+    const T* x = static_cast<const T*>(m.data);
+    const int col = c0 + lane * 8;
+    at.load(x + row * m.ld + col, col < cols, x, x + (rows - 1) * m.ld + cols);
+  }
+  __device__ __forceinline__ void widen(float (&x)[8], int col, int cols) const {
+    uint32_t w[2 * sizeof(T)];
+    at.words(w);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if constexpr (sizeof(T) == 4)
+        x[i] = __uint_as_float(w[i]), x[i + 1] = __uint_as_float(w[i + 1]);
+      else
+        unpack2(w[i / 2], x[i], x[i + 1], T());
+    }
+    if (col + 8 > cols) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i >= cols) x[i] = 0.f;
+    }
+  }
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void unit_store(const Mat& m, int64_t row, int lane, int cols, int c0,
+                                           const float (&f)[8]) {
+  if constexpr (VEC) {
+    frag_store<T, true>(m, row, 0, lane, 32, cols, f, c0);
+  } else {
+    const int col = c0 + lane * 8;
+    uint32_t w[2 * sizeof(T)];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(f[i]), w[i + 1] = __float_as_uint(f[i + 1]);
+      else
+        w[i / 2] = pack2(f[i], f[i + 1], T());
+    }
+    store_window<8 * (int)sizeof(T), (int)sizeof(T)>(
+        static_cast<T*>(m.data) + row * m.ld + col, w, lane,
+        ((int64_t)cols - col) * (int64_t)sizeof(T));
+  }
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ void unit_pack(const Act8Out& o, int64_t row, int lane, int cols, int c0,
+                                          const float (&f)[8]) {
+  if constexpr (VEC) {
+    act8_store8<T>(o, row, c0 + lane * 8, cols, f);
+  } else {
+    const int col = c0 + lane * 8;
+    uint32_t w[2];
+    const uint32_t byte = act8_codes8<T>(f, w[0], w[1]);
+    store_window<8, 1>(o.codes + row * o.ld_codes + col, w, lane, (int64_t)cols - col);
+    if (col < cols && (lane & 3) == 0) o.exps[row * o.ld_exps + col / kAct8Block] = (uint8_t)byte;
+  }
+}
+
+// A packed unit on its way to values, laid out alike; from cols on the values mean
+// nothing.
+template <bool VEC>
+struct CodeFrag {
+  uint2 c;
+  Window<8, 1> at;  // VEC: unused
+  uint32_t byte;
+  __device__ __forceinline__ void load(const Act8Out& o, int64_t rows, int64_t row, int lane,
+                                       int cols, int c0) {
+    const int col = c0 + lane * 8;
+    const int8_t* p = o.codes + row * o.ld_codes + col;
+    if constexpr (VEC) {
+      c = make_uint2(0, 0);
+      if (col < cols) c = *reinterpret_cast<const uint2*>(p);
+    } else {
+      at.load(p, col < cols, o.codes, o.codes + (rows - 1) * o.ld_codes + cols);
+    }
+    byte = col < cols ? o.exps[row * o.ld_exps + col / kAct8Block] : 0;
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    if constexpr (VEC) {
+      act8_values(c, act8_scale(byte), f);
+    } else {
+      uint32_t w[2];
+      at.words(w);
+      act8_values(make_uint2(w[0], w[1]), act8_scale(byte), f);
+    }
   }
 };
 
