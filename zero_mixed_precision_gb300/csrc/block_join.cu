@@ -253,6 +253,8 @@ struct JoinGradParams {
   float res_scale, branch_scale;
   int64_t gate_rows;
   int by_gate;  // the finish kernel's sums of dgate: by gate row, or by part
+  int gate_few;                     // each of few parts
+  unsigned weight_ctas, gate_ctas;  // CTAs of one of its sums over all parts, of dgate's
   Mat dh_out, du, y, h_out, gate, dh, dy, dgate;
   Act8Out y8, h8;
   const void *w_post, *w_pre;
@@ -588,15 +590,72 @@ __device__ __forceinline__ void stage_typed_grad(const JoinGradParams& p, int64_
       q[(v * 8 + i) * stride] = p.branch_scale * to_f32(rb[v][i]) * to_f32(rg[v][i]);
     }
 }
+// Eight parameters, or eight of a partial row, which the finish kernel reads next.  (As
+// inline assembly in two branches nvcc 13.0.88 fails on these.)
+template <class W>
+__device__ __forceinline__ void st_param8(W* p, const float (&f)[8]) {
+  if constexpr (sizeof(W) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1], W()), pack2(f[2], f[3], W()),
+                                              pack2(f[4], f[5], W()), pack2(f[6], f[7], W()));
+  }
+}
+template <class W>
+__device__ __forceinline__ Raw8<W> ld_param8(const W* p) {
+  Raw8<W> r;
+  r.v = *reinterpret_cast<const uint4*>(p);
+  if constexpr (sizeof(W) == 4) r.w = *reinterpret_cast<const uint4*>(p + 4);
+  return r;
+}
+
+// The same by 16 bytes, where the parameters' rows are aligned like the matrices'.
+template <class W, int NV>
+__device__ __forceinline__ bool stage_wide_grad(const JoinGradParams& p, int64_t grow, int t,
+                                                float* wpre, float* q, int stride) {
+  const W* a = wpre ? static_cast<const W*>(p.w_pre) : nullptr;
+  const W* b = static_cast<const W*>(p.w_post);
+  const W* g = p.gate.data ? static_cast<const W*>(p.gate.data) + grow * p.gate.ld : nullptr;
+  if (((uintptr_t)a | (uintptr_t)b | (uintptr_t)g) & 15) return false;
+  Raw8<W> ra[NV] = {}, rb[NV] = {}, rg[NV] = {};
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = min(column<true>(v, 0, t, p.tpr), p.cols - 8);
+    if (a) ra[v] = ld_param8<W>(a + c);
+    if (b) rb[v] = ld_param8<W>(b + c);
+    if (g) rg[v] = ld_param8<W>(g + c);
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    float fa[8], fb[8], fg[8];
+    widen8<W>(ra[v], fa);
+    widen8<W>(rb[v], fb);
+    widen8<W>(rg[v], fg);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (wpre) wpre[(v * 8 + i) * stride] = a ? fa[i] : 1.f;
+      q[(v * 8 + i) * stride] = p.branch_scale * (b ? fb[i] : 1.f) * (g ? fg[i] : 1.f);
+    }
+  }
+  return true;
+}
+template <class W, bool VEC, int NV>
+__device__ __forceinline__ void stage_any_grad(const JoinGradParams& p, int64_t grow, int t,
+                                               float* wpre, float* q, int stride) {
+  if constexpr (VEC)
+    if (stage_wide_grad<W, NV>(p, grow, t, wpre, q, stride)) return;
+  stage_typed_grad<W, VEC, NV>(p, grow, t, wpre, q, stride);
+}
 template <bool VEC, int NV>
 __device__ __noinline__ void stage_grad(const JoinGradParams& p, int64_t grow, int t, float* wpre,
                                         float* q, int stride) {
   if (p.param_dtype == DPOPT_GRAD_BF16)
-    stage_typed_grad<bf16, VEC, NV>(p, grow, t, wpre, q, stride);
+    stage_any_grad<bf16, VEC, NV>(p, grow, t, wpre, q, stride);
   else if (p.param_dtype == DPOPT_GRAD_F16)
-    stage_typed_grad<fp16, VEC, NV>(p, grow, t, wpre, q, stride);
+    stage_any_grad<fp16, VEC, NV>(p, grow, t, wpre, q, stride);
   else
-    stage_typed_grad<float, VEC, NV>(p, grow, t, wpre, q, stride);
+    stage_any_grad<float, VEC, NV>(p, grow, t, wpre, q, stride);
 }
 
 // At the end of a gate row's rows in a part: its sums branch_scale * e (in `mine`)
@@ -633,21 +692,66 @@ __device__ __forceinline__ void close_typed(const JoinGradParams& p, bool inside
     }
 }
 
+// The same by 16 bytes, as above.
+template <class W, int NV>
+__device__ __forceinline__ bool close_wide(const JoinGradParams& p, bool inside, int64_t grow,
+                                           float* out, int t, float* post, const float* mine,
+                                           int stride) {
+  const W* gate = p.gate.data ? static_cast<const W*>(p.gate.data) + grow * p.gate.ld : nullptr;
+  const W* wpost = static_cast<const W*>(p.w_post);
+  W* dgate = p.dgate.data ? static_cast<W*>(p.dgate.data) + grow * p.dgate.ld : nullptr;
+  if (((uintptr_t)gate | (uintptr_t)wpost | (uintptr_t)dgate) & 15) return false;
+  Raw8<W> rg[NV] = {}, rw[NV] = {};
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = min(column<true>(v, 0, t, p.tpr), p.cols - 8);
+    if (gate) rg[v] = ld_param8<W>(gate + c);
+    if (wpost) rw[v] = ld_param8<W>(wpost + c);
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = column<true>(v, 0, t, p.tpr);
+    if (c >= p.cols) continue;
+    float g[8], w[8];
+    widen8<W>(rg[v], g);
+    widen8<W>(rw[v], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& sum = post[(v * 8 + i) * stride];
+      const float x = mine[(v * 8 + i) * stride];
+      sum = fmaf(gate ? g[i] : 1.f, x, sum);
+      w[i] = (wpost ? w[i] : 1.f) * x;
+    }
+    if (!dgate) continue;
+    if (inside)
+      st_param8(dgate + c, w);
+    else
+      st_param8(out + c, w);
+  }
+  return true;
+}
+template <class W, bool VEC, int NV>
+__device__ __forceinline__ void close_any(const JoinGradParams& p, bool inside, int64_t grow,
+                                          float* out, int t, float* post, const float* mine,
+                                          int stride) {
+  if constexpr (VEC)
+    if (close_wide<W, NV>(p, inside, grow, out, t, post, mine, stride)) return;
+  close_typed<W, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+}
+
 template <bool VEC, int NV>
 __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t part, int64_t lo,
-                                            int64_t hi, int64_t row, bool first_gate, int t,
+                                            int64_t hi, int64_t grow, bool first_gate, int t,
                                             float* post, const float* mine, int stride) {
-  int64_t glo, ghi;
-  gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
-  const bool inside = glo >= lo && ghi <= hi;
-  const int64_t grow = gate_row_of(p.gate_rows, row);
+  const int64_t glo = grow * p.gate_rows;
+  const bool inside = glo >= lo && min(p.rows, glo + p.gate_rows) <= hi;
   float* out = part_row(p, part, first_gate ? kPartGateFirst : kPartGateLast);
   if (p.param_dtype == DPOPT_GRAD_BF16)
-    close_typed<bf16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+    close_any<bf16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
   else if (p.param_dtype == DPOPT_GRAD_F16)
-    close_typed<fp16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+    close_any<fp16, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
   else
-    close_typed<float, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
+    close_any<float, VEC, NV>(p, inside, grow, out, t, post, mine, stride);
 }
 
 // One CTA per run of rows.  Per row one reading forms three sums,
@@ -662,8 +766,9 @@ __device__ __noinline__ void close_gate_row(const JoinGradParams& p, int64_t par
 // arithmetic, half of it restoring the codes twice, takes longer than the memory.
 // Whole rows by bulk copies in place of the threads' own measured the same from
 // 8 bits and slower from 16 (337 us); CTAs of 1024 threads of half the columns 486 us, of 256
-// with twice the columns 357 us.  8192 x 2048 from 8 bits 57 us, of which 8 are
-// the final sums.
+// with twice the columns 357 us.  8192 x 2048 from 8 bits 50 us, of which 8 are
+// the final sums; 3330 x 1920 with a gate row per row 41 us (72 with parameters read
+// one by one).
 template <class T, bool VEC, class Rows>
 __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
     block_join_grad_kernel(const __grid_constant__ JoinGradParams p) {
@@ -708,6 +813,12 @@ __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
           const int at = (v * 8 + 2 * i) * tpr;
           q[v][i] = pair(mine[at], mine[at + tpr]);
         }
+    }
+    if (row + 1 == gate_end && row + 1 < hi && p.gate.data) {  // the next gate row on its way
+      const char* next = static_cast<const char*>(p.gate.data) +
+                         (grow + 1) * p.gate.ld * (p.param_dtype == DPOPT_GRAD_F32 ? 4 : 2);
+      for (int b = t * 128; b < p.cols * 2; b += tpr * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + b));
     }
     in.begin();
     const float r1 = in.r1, r2 = in.r2;
@@ -777,50 +888,76 @@ __global__ void __launch_bounds__(Rows::kMaxThreads, 1)
           mine[at + tpr] = p.branch_scale * lane1(e[v][i]);
           e[v][i] = 0;
         }
-      close_gate_row<VEC, NV>(p, blockIdx.x, lo, hi, row, first_gate, t, post, mine, tpr);
+      close_gate_row<VEC, NV>(p, blockIdx.x, lo, hi, grow, first_gate, t, post, mine, tpr);
       first_gate = false;
       new_gate = true;
       ++grow;
       gate_end = min(hi, gate_end + p.gate_rows);
     }
   }
+  if constexpr (VEC) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(v, i, t, tpr);
+    for (int v = 0; v < NV; ++v) {
+      const int c = column<true>(v, 0, t, tpr);
       if (c >= p.cols) continue;
-      if (p.dw_pre)
-        part_row(p, blockIdx.x, kPartWPre)[c] = i & 1 ? lane1(acc[v][i / 2]) : lane0(acc[v][i / 2]);
-      const float x = i & 1 ? lane1(e[v][i / 2]) : lane0(e[v][i / 2]);
-      part_row(p, blockIdx.x, kPartWPost)[c] =
-          p.gate_rows == 0 ? p.branch_scale * x : post[(v * 8 + i) * tpr];
+      float x[8];
+      if (p.dw_pre) {
+        lanes8(acc[v], x);
+        st_param8(part_row(p, blockIdx.x, kPartWPre) + c, x);
+      }
+      lanes8(e[v], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = p.gate_rows == 0 ? p.branch_scale * x[i] : post[(v * 8 + i) * tpr];
+      st_param8(part_row(p, blockIdx.x, kPartWPost) + c, x);
     }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = column<VEC>(v, i, t, tpr);
+        if (c >= p.cols) continue;
+        if (p.dw_pre)
+          part_row(p, blockIdx.x, kPartWPre)[c] = i & 1 ? lane1(acc[v][i / 2]) : lane0(acc[v][i / 2]);
+        const float x = i & 1 ? lane1(e[v][i / 2]) : lane0(e[v][i / 2]);
+        part_row(p, blockIdx.x, kPartWPost)[c] =
+            p.gate_rows == 0 ? p.branch_scale * x : post[(v * 8 + i) * tpr];
+      }
+  }
 }
 
-// Adds the parts' partial rows.  blockIdx.y: 0 dw_pre; 1 dw_post (with one gate row
-// for all rows the sums e, from which dw_post = gate e and dgate = w_post e); from 2 on
-// the gate rows that cross a part's border: gate row blockIdx.y - 2 (when there are
-// fewer gate rows than parts), or the one that begins in part blockIdx.y - 2 and
-// reaches into the next.  32 columns x 32 runs of parts per CTA; a run adds its
-// parts in order, then the runs' sums are added in order.
-constexpr int kFinishRuns = 32;
+// Adds the parts' partial rows.  Sum 0 is dw_pre; 1 dw_post (with one gate row for all
+// rows the sums e, from which dw_post = gate e and dgate = w_post e); from 2 on the
+// gate rows that cross a part's border: gate row `sum` - 2 (when there are fewer gate
+// rows than parts), or the one that begins in part `sum` - 2 and reaches into the
+// next.  Of many parts a CTA adds 32 columns in 32 runs: a run adds its parts in order,
+// then the runs' sums are added in order.  Of at most kFinishFew each thread adds a
+// column's (15 x 6965, a gate row per two rows: 32 runs for each of its 2180 pieces
+// of a sum made the gradient 40 us).
+constexpr int kFinishRuns = 32, kFinishFew = 16;
 
 __global__ void __launch_bounds__(32 * kFinishRuns)
     block_join_finish_kernel(const __grid_constant__ JoinGradParams p) {
   pdl_enter();
   __shared__ float run_sum[kFinishRuns][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const unsigned weights = 2 * p.weight_ctas;
+  const bool of_gate = blockIdx.x >= weights;
+  const unsigned ctas = of_gate ? p.gate_ctas : p.weight_ctas;  // of a sum
+  const unsigned k = of_gate ? blockIdx.x - weights : blockIdx.x;
+  const int sum = (int)(k / ctas) + (of_gate ? 2 : 0);
+  const bool few = of_gate ? p.gate_few : p.parts <= kFinishFew;
+  const int col = (int)(k % ctas) * (few ? 32 * kFinishRuns : 32) + (few ? threadIdx.x : lane);
   const int64_t parts = p.parts, per = p.per;
   int64_t first = 0, last = parts, out_row = 0;  // parts [first, last)
-  int slot = blockIdx.y, first_slot = slot;
-  const bool both = blockIdx.y == 1 && p.gate_rows == 0;
-  bool wanted = blockIdx.y == 0 ? p.dw_pre != nullptr
-                                : p.dw_post != nullptr || (both && p.dgate.data != nullptr);
-  if (blockIdx.y >= 2) {
+  int slot = sum, first_slot = slot;
+  const bool both = sum == 1 && p.gate_rows == 0;
+  bool wanted = sum == 0 ? p.dw_pre != nullptr
+                         : p.dw_post != nullptr || (both && p.dgate.data != nullptr);
+  if (sum >= 2) {
     slot = first_slot = kPartGateFirst;
-    const int64_t q = blockIdx.y - 2;
+    const int64_t q = sum - 2;
     const int64_t row = p.by_gate ? q * p.gate_rows : min(p.rows, (q + 1) * per) - 1;
     int64_t glo, ghi;
     gate_span(p.gate_rows, p.rows, row, &glo, &ghi);
@@ -833,8 +970,8 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
   }
   if (!wanted) return;
   float s = 0.f;
-  const int64_t each = (last - first + kFinishRuns - 1) / kFinishRuns;
-  int64_t a = first + run * each;
+  const int64_t each = few ? last - first : (last - first + kFinishRuns - 1) / kFinishRuns;
+  int64_t a = first + (few ? 0 : run * each);
   const int64_t b = min(last, a + each);
   if (col < p.cols && a < b) {
     const float* at = part_row(p, a, a == first ? first_slot : slot) + col;
@@ -843,12 +980,15 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
 #pragma unroll 8
     for (++a; a < b; ++a, at += kPartSlots * p.width) s += *at;
   }
-  run_sum[run][lane] = s;
-  __syncthreads();
-  if (run != 0 || col >= p.cols) return;
+  if (!few) {
+    run_sum[run][lane] = s;
+    __syncthreads();
+    if (run != 0) return;
 #pragma unroll
-  for (int i = 1; i < kFinishRuns; ++i) s += run_sum[i][lane];
-  if (blockIdx.y == 0) {
+    for (int i = 1; i < kFinishRuns; ++i) s += run_sum[i][lane];
+  }
+  if (col >= p.cols) return;
+  if (sum == 0) {
     st_any(p.dw_pre, p.param_dtype, col, s);
   } else if (both) {
     if (p.dw_post)
@@ -857,7 +997,7 @@ __global__ void __launch_bounds__(32 * kFinishRuns)
     if (p.dgate.data)
       st_any(p.dgate.data, p.param_dtype, col,
              p.w_post ? s * ld_any(p.w_post, p.param_dtype, col) : s);
-  } else if (blockIdx.y == 1) {
+  } else if (sum == 1) {
     st_any(p.dw_post, p.param_dtype, col, s);
   } else {
     st_any(p.dgate.data, p.param_dtype, out_row * p.dgate.ld + col, s);
@@ -1173,8 +1313,15 @@ int dpopt_block_join_backward(const dpopt_block_join_grad_args* a, dpopt_stream_
   }
   if (!p.dw_pre && !p.dw_post && gate_sums == 0 && !(p.dgate.data && a->gate_rows == 0))
     return DPOPT_OK;
-  const dim3 grid((unsigned)((cols + 31) / 32), 2 + gate_sums);
-  return launched(launch_pdl(block_join_finish_kernel, grid, dim3(32 * kFinishRuns), 0,
+  const auto ctas = [&](bool few) {
+    const int64_t each = few ? 32 * kFinishRuns : 32;
+    return (unsigned)((cols + each - 1) / each);
+  };
+  p.gate_few = a->gate_rows / p.per + 2 <= kFinishFew;
+  p.weight_ctas = ctas(parts <= kFinishFew);
+  p.gate_ctas = ctas(p.gate_few);
+  const unsigned grid = 2 * p.weight_ctas + gate_sums * p.gate_ctas;
+  return launched(launch_pdl(block_join_finish_kernel, grid, 32 * kFinishRuns, 0,
                              (cudaStream_t)stream, p),
                   "block join gradient sums");
 }
