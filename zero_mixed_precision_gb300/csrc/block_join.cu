@@ -63,6 +63,26 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr
   }
 }
 
+// Eight parameters, or eight of a partial row, which the finish kernel reads next.  (As
+// inline assembly in two branches nvcc 13.0.88 fails on these.)
+template <class W>
+__device__ __forceinline__ void st_param8(W* p, const float (&f)[8]) {
+  if constexpr (sizeof(W) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1], W()), pack2(f[2], f[3], W()),
+                                              pack2(f[4], f[5], W()), pack2(f[6], f[7], W()));
+  }
+}
+template <class W>
+__device__ __forceinline__ Raw8<W> ld_param8(const W* p) {
+  Raw8<W> r;
+  r.v = *reinterpret_cast<const uint4*>(p);
+  if constexpr (sizeof(W) == 4) r.w = *reinterpret_cast<const uint4*>(p + 4);
+  return r;
+}
+
 // Values of a parameter (row `at` elements in; ones where it is absent) at a
 // thread's columns, into its places out[i * stride].  Not inlined: parameters are
 // read once per launch or gate row, and their three types and eight addresses
@@ -71,6 +91,21 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*slot)[N], int tpr
 template <class W, bool VEC, int NV>
 __device__ __forceinline__ void stage_typed(const W* w, int t, int tpr, int cols, float* out,
                                             int stride) {
+  if constexpr (VEC) {
+    if ((uintptr_t)w % 16 == 0) {  // so are whole fragments
+      Raw8<W> r[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) r[v] = ld_param8(w + min(column<true>(v, 0, t, tpr), cols - 8));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+        widen8<W>(r[v], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[(v * 8 + i) * stride] = f[i];
+      }
+      return;
+    }
+  }
   W raw[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -130,17 +165,22 @@ __global__ void __launch_bounds__(TPR == 0 ? kRowCta : TPR < 512 ? 512 : TPR, 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) wpre[v][i] = mine[(v * 8 + i) * tpr];
   Frag<T, VEC> fh[NV], fy[NV];
-  int64_t row = blockIdx.x;
+  // With gate rows a CTA takes a run of rows, so that it changes its gate row as
+  // seldom as can be (8192 x 4096, one per 64 rows: 97 us with every grid-th row).
+  const bool run = p.gate_rows > 0;
+  int64_t row = run ? (int64_t)blockIdx.x * p.rows / gridDim.x : blockIdx.x;
+  const int64_t end = run ? ((int64_t)blockIdx.x + 1) * p.rows / gridDim.x : p.rows;
+  const int64_t step = run ? 1 : gridDim.x;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     fh[v].load(p.h, row, v, t, tpr, cols);
     fy[v].load(p.y, row, v, t, tpr, cols);
   }
-  int64_t held = -1;  // gate row in pb
-  for (; row < p.rows; row += gridDim.x) {
-    const int64_t grow = gate_row_of(p.gate_rows, row);
-    if (grow != held) {
-      held = grow;
+  int64_t gate_end = 0;  // the gate row in pb holds below it
+  for (; row < end; row += step) {
+    if (row >= gate_end) {
+      const int64_t grow = gate_row_of(p.gate_rows, row);
+      gate_end = run ? (grow + 1) * p.gate_rows : INT64_MAX;
       stage_param<VEC, NV>(p.w_post, p.param_dtype, 0, t, tpr, cols, mine, tpr);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -156,12 +196,12 @@ __global__ void __launch_bounds__(TPR == 0 ? kRowCta : TPR < 512 ? 512 : TPR, 1)
       }
     }
     float h[NV][8], y[NV][8];
-    const int64_t next = row + gridDim.x;
+    const int64_t next = row + step;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       fh[v].widen(h[v]);
       fy[v].widen(y[v]);
-      if (next < p.rows) {
+      if (next < end) {
         fh[v].load(p.h, next, v, t, tpr, cols);
         fy[v].load(p.y, next, v, t, tpr, cols);
       }
@@ -590,26 +630,6 @@ __device__ __forceinline__ void stage_typed_grad(const JoinGradParams& p, int64_
       q[(v * 8 + i) * stride] = p.branch_scale * to_f32(rb[v][i]) * to_f32(rg[v][i]);
     }
 }
-// Eight parameters, or eight of a partial row, which the finish kernel reads next.  (As
-// inline assembly in two branches nvcc 13.0.88 fails on these.)
-template <class W>
-__device__ __forceinline__ void st_param8(W* p, const float (&f)[8]) {
-  if constexpr (sizeof(W) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1], W()), pack2(f[2], f[3], W()),
-                                              pack2(f[4], f[5], W()), pack2(f[6], f[7], W()));
-  }
-}
-template <class W>
-__device__ __forceinline__ Raw8<W> ld_param8(const W* p) {
-  Raw8<W> r;
-  r.v = *reinterpret_cast<const uint4*>(p);
-  if constexpr (sizeof(W) == 4) r.w = *reinterpret_cast<const uint4*>(p + 4);
-  return r;
-}
-
 // The same by 16 bytes, where the parameters' rows are aligned like the matrices'.
 template <class W, int NV>
 __device__ __forceinline__ bool stage_wide_grad(const JoinGradParams& p, int64_t grow, int t,
