@@ -111,6 +111,18 @@ def test_given_tokens_and_alternatives(dp, n, top):
                 _check_backward(dp, x, tok, o, entropy=entropy)
 
 
+@pytest.mark.parametrize("vocab", [32, 255, 256, 257, 640, 1024, 1025, 1500, 2048])
+def test_alternatives_of_short_rows(dp, vocab):
+    """Rows that do not reach every thread: most or all of their logits are candidates."""
+    for dtype in DTYPES:
+        x, g = _logits(6, vocab, dtype, seed=vocab)
+        x[1] = x[1].round()       # few distinct logits
+        x[2, 5:] = -math.inf      # fewer than are asked for
+        tok = _tokens(g, 6, 1, vocab)
+        for top in (17, 32):
+            _check_forward(dp, x, tok, top=top)
+
+
 @pytest.mark.parametrize("inv_temp", [0.5, 1.25, 3.0])
 @pytest.mark.parametrize("scale", [None, 1.0, 1024.0])
 def test_temperature_and_loss_scale(dp, inv_temp, scale):

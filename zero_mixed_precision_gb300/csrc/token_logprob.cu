@@ -196,6 +196,8 @@ __device__ __forceinline__ TokPartial lanes_merge(TokPartial p, int lanes) {
   return p;
 }
 
+constexpr int kTokCand = 1024;  // candidates a stretch lists; a multiple of kTokThreads
+
 struct TokShared {
   TokPartial part[kTokWarps];
   float slot[kTokWarps];
@@ -203,7 +205,7 @@ struct TokShared {
   uint32_t group[32], floor;
   int found, agains;
   uint16_t again[kTokThreads];
-  uint64_t cand[1024];
+  uint64_t cand[kTokCand], kgroup[32], kfloor;
   uint64_t best[DPOPT_MAX_TOP];
 };
 
@@ -235,7 +237,7 @@ struct Stretch {
 
 // K = 1 .. top largest of the keys a thread can list, by `top` passes over
 // them: each pass takes the largest below the last.  The form for rows whose
-// candidates are too many for the list (few distinct or few unmasked logits).
+// candidates are many (short ones; few distinct or few unmasked logits).
 template <class F>
 __device__ __forceinline__ void top_by_passes(int top, uint64_t* best, TokShared& sh, F each) {
   uint64_t last = ~0ull;
@@ -282,36 +284,82 @@ __device__ void stretch_top(const Stretch<T>& st, int64_t lo, int top, float thr
   auto offer = [&](float x, int64_t i) {
     if (x < floor_value) return;
     const int n = atomicAdd(&sh.found, 1);  // the order in the list does not matter
-    if (n < (int)(sizeof(sh.cand) / 8)) sh.cand[n] = rank_key(x, (uint32_t)(lo + i));
+    if (n < kTokCand) sh.cand[n] = rank_key(x, (uint32_t)(lo + i));
   };
   // the threads to look at again, then a warp for each: lane i takes the thread's
-  // i-th vector, so that they are all in flight at once
-  if (mine >= floor) sh.again[atomicAdd(&sh.agains, 1)] = (uint16_t)threadIdx.x;
+  // i-th vector, so that they are all in flight at once; or each thread its own
+  // vectors, where they are fewer than the threads that a warp would take in turn (13 x
+  // 1024 with 20 alternatives, where all threads look again: 22 us by warps, 5 like this)
+  const bool again = mine >= floor;
+  if (again) sh.again[atomicAdd(&sh.agains, 1)] = (uint16_t)threadIdx.x;
   __syncthreads();
   const int agains = sh.agains, lane = threadIdx.x & 31;
-  for (int a = threadIdx.x >> 5; a < agains; a += kTokWarps) {
-    const int64_t t = sh.again[a];
-    if (lane == 0 && t < st.loose()) offer(to_f32(st.x[st.loose_at(t)]), st.loose_at(t));
-    for (int64_t v = t + lane * kTokThreads; v < st.vecs; v += 32 * kTokThreads) {
-      float f[8];
-      widen8<T>(ld_raw8<T>(st.x + st.head + v * 8), f);
+  auto offer8 = [&](int64_t v) {
+    float f[8];
+    widen8<T>(ld_raw8<T>(st.x + st.head + v * 8), f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) offer(f[i], st.head + v * 8 + i);
+    for (int i = 0; i < 8; ++i) offer(f[i], st.head + v * 8 + i);
+  };
+  if (st.vecs / kTokThreads < agains / kTokWarps) {
+    if (again) {
+      if (threadIdx.x < st.loose())
+        offer(to_f32(st.x[st.loose_at(threadIdx.x)]), st.loose_at(threadIdx.x));
+      for (int64_t v = threadIdx.x; v < st.vecs; v += kTokThreads) offer8(v);
+    }
+  } else {
+    for (int a = threadIdx.x >> 5; a < agains; a += kTokWarps) {
+      const int64_t t = sh.again[a];
+      if (lane == 0 && t < st.loose()) offer(to_f32(st.x[st.loose_at(t)]), st.loose_at(t));
+      for (int64_t v = t + lane * kTokThreads; v < st.vecs; v += 32 * kTokThreads) offer8(v);
     }
   }
   __syncthreads();
-  const int n = sh.found;
-  if (n <= (int)(sizeof(sh.cand) / 8)) {
+  int n = sh.found;
+  if (n > kTokThreads && n <= kTokCand) {
+    // many: a short row, whose vectors do not reach every group.  The keys sift
+    // themselves in the same way (all of 13 x 1024 ranked at once: 50 us)
+    uint64_t k[kTokCand / kTokThreads], most = 0;
+#pragma unroll
+    for (int u = 0; u < kTokCand / kTokThreads; ++u) {
+      const int i = threadIdx.x + u * kTokThreads;
+      k[u] = i < n ? sh.cand[i] : 0;
+      most = max(most, k[u]);
+    }
+#pragma unroll
+    for (int o = 1; o < kGroup32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (threadIdx.x % kGroup32 == 0) sh.kgroup[threadIdx.x / kGroup32] = most;
+    __syncthreads();  // every key is in registers: the list may be written again
+    if (threadIdx.x == 0) sh.found = 0;
+    if (threadIdx.x < 32) {
+      most = sh.kgroup[threadIdx.x];
+      int rank = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) rank += __shfl_sync(0xffffffffu, most, j) > most;
+      if (rank == top - 1) sh.kfloor = most;  // the keys are distinct, no group is empty
+    }
+    __syncthreads();
+    const uint64_t kfloor = sh.kfloor;
+#pragma unroll
+    for (int u = 0; u < kTokCand / kTokThreads; ++u)
+      if (k[u] >= kfloor) sh.cand[atomicAdd(&sh.found, 1)] = k[u];
+    __syncthreads();
+    n = sh.found;
+  }
+  if (n <= kTokThreads) {
     // a candidate's place is the number of larger ones (keys are distinct)
     for (int i = threadIdx.x; i < top; i += kTokThreads)
       if (i >= n) sh.best[i] = 0;
-    for (int i = threadIdx.x; i < n; i += kTokThreads) {
-      const uint64_t k = sh.cand[i];
+    if ((int)threadIdx.x < n) {
+      const uint64_t k = sh.cand[threadIdx.x];
       int above = 0;
       for (int j = 0; j < n; ++j) above += sh.cand[j] > k;
       if (above < top) sh.best[above] = k;
     }
     __syncthreads();
+  } else if (n <= kTokCand) {
+    top_by_passes(top, sh.best, sh, [&](auto take) {
+      for (int i = threadIdx.x; i < n; i += kTokThreads) take(sh.cand[i]);
+    });
   } else {
     top_by_passes(top, sh.best, sh, [&](auto take) {
       for (int64_t j = threadIdx.x; j < st.len; j += kTokThreads)
